@@ -62,7 +62,9 @@ typedef enum {
   BITNET_ERR_UNSUPPORTED = 5,  /* device is not sm_100 / feature unavailable  */
   BITNET_ERR_CUDA = 6,         /* a CUDA runtime call failed                  */
   BITNET_ERR_TIMEOUT = 7,      /* a device-side bounded wait gave up          */
-  BITNET_ERR_NONFINITE = 8     /* a weight was Inf or NaN (gamma set to NaN)  */
+  BITNET_ERR_NONFINITE = 8,    /* a weight was Inf or NaN (gamma set to NaN)  */
+  BITNET_ERR_PAGES = 9         /* device side: a slot, length or page outside the
+                                  cache's tables, or too few free pages         */
 } bitnet_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -453,9 +455,190 @@ BITNET_API bitnet_status bitnet_ffn_tp_finish(const int32_t* acc, int64_t M, int
                                               float eps, uint16_t* y, float* y_f32, void* stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Attention and its key-value cache: what stands in a decoder layer between
+ * the query/key/value projections (bitnet_linear_multi) and the output
+ * projection (bitnet_linear).  [A] section "モデル構造" (LLaMA-like decoder
+ * layers); [Y] section "BitAttentionとMGQA" (query heads that share key-value
+ * heads).  Forward pass only, like the rest of the library; positions (RoPE)
+ * are the caller's.
+ *
+ * Shared rules.  Queries, keys and values are bf16 bits; Hq query heads, Hkv
+ * key-value heads, query head h reads key-value head h / (Hq / Hkv).
+ * Requires D = 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 64, Hq <= 65536.
+ * Token strides are in elements, at least heads * D and multiples of 8 (so
+ * that q, k and v may be slices of one fused projection).  scale is finite
+ * and > 0.  Scores, maxima, sums and outputs are fp32; probabilities are
+ * rounded to bf16 for the product with the values; y is rounded once.
+ * A row that sees no key gives y = 0 and lse = -inf (likewise one whose
+ * scores are all -inf).  Keys and values that a row does not see do not reach
+ * it, whatever they hold (Inf and NaN included).
+ * lse (optional, fp32, contiguous) is the natural logarithm of
+ * sum_j exp(scale * q . k_j).
+ */
+
+/*
+ * Causal attention over packed prompts.
+ * q [Tq, Hq, D], k and v [Tk, Hkv, D], y [Tq, Hq, D] with token strides
+ * q_stride, k_stride, v_stride, y_stride; lse [Tq, Hq] or NULL.
+ * cu_q, cu_k   [B+1] int32 on the device: sequence i has rows cu_q[i] ..
+ *          cu_q[i+1]-1 and keys cu_k[i] .. cu_k[i+1]-1.  With ql rows and kl
+ *          keys, row r (from 0) sees keys 0 .. r + kl - ql: a whole prompt has
+ *          ql == kl (pass the same array twice), a later piece of a prompt
+ *          ql < kl; with ql > kl the first ql - kl rows see nothing.  Sequences
+ *          may be empty.  Rows outside all sequences (before the first, behind
+ *          the last) are neither read nor written.
+ * A sequence whose bounds are not inside [0, Tq] and [0, Tk] or decrease is
+ * skipped and BITNET_ERR_INVALID_ARG goes to the device status word.
+ * Requires 1 <= B, Tq, Tk < 2^30.  y may not overlap q, k or v
+ * (BITNET_ERR_INVALID_ARG).  No workspace.
+ */
+BITNET_API bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride,
+                                            const uint16_t* k, int64_t k_stride,
+                                            const uint16_t* v, int64_t v_stride,
+                                            const int32_t* cu_q, const int32_t* cu_k, int64_t B,
+                                            int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
+                                            int64_t D, float scale, uint16_t* y,
+                                            int64_t y_stride, float* lse, void* stream);
+
+/*
+ * A paged key-value cache.  Sequences live in slots; a slot's tokens lie in
+ * pages of page_size tokens, named by its row of the table in order.  The
+ * tables serve all layers; each layer has its own pages
+ *   k_pages, v_pages  [n_pages, Hkv, page_size, D] bf16 bits.
+ * table   [n_slots, max_pages] int32: page of each entry, -1 where none.
+ * lens    [n_slots] int32: tokens held (a slot of length 0 holds no pages).
+ * refs    [n_pages] int32: table entries that name the page; 0 = free.
+ * An empty cache has table = -1, lens = 0, refs = 0.  The three arrays are on
+ * the device (4-byte aligned); the struct itself is on the host and read
+ * during the call only.  1 <= n_slots <= 65536, page_size a multiple of 16
+ * in 16 .. 1024, n_pages <= 2^30, max_pages * page_size < 2^30.
+ *
+ * Every decision is made on the device, so a captured call replays on what
+ * the tables hold then.  Pages are taken lowest index first, in the order of
+ * the request: results are a function of the tables alone.  Calls that change
+ * the same tables must be ordered by the caller (one stream).  What a call
+ * finds wrong in device data (a slot outside the tables, a length that does
+ * not fit, a page outside the pool, too few free pages) goes to the device
+ * status word as BITNET_ERR_PAGES; no call reads or writes outside the arrays
+ * for it.
+ */
+typedef struct {
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int64_t n_slots, max_pages, n_pages, page_size;
+} bitnet_kv_tables;
+
+/* Scratch of bitnet_kv_extend, _fork and _compact (bytes). */
+BITNET_API size_t bitnet_kv_workspace_size(int64_t n_slots, int64_t n_pages);
+
+/*
+ * Grow n sequences: slot slots[i] (NULL: i) by add[i] >= 0 tokens.  Entries
+ * of the new tokens that name no page get a free one, lens[slot] += add[i].
+ * A slot may be named once.  All or nothing: with bad arguments or too few
+ * free pages nothing changes.
+ * short_pages  one int32 on the device or NULL: 0 when done, the number of
+ *          pages that were lacking, or -1 for bad arguments (an unknown or
+ *          repeated slot, add < 0, more than max_pages * page_size tokens).
+ */
+BITNET_API bitnet_status bitnet_kv_extend(const bitnet_kv_tables* kv, const int32_t* slots,
+                                          const int32_t* add, int64_t n, int32_t* short_pages,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Write the newest rows of B sequences into one layer's pages.  Batch row b
+ * has rows cu[b] .. cu[b+1]-1 of k and v [T, Hkv, D] (token strides k_stride,
+ * v_stride), the last tokens of slot slots[b] (NULL: b): row r goes to
+ * position lens[slot] - (cu[b+1] - cu[b]) + r - cu[b].  Call it after
+ * bitnet_kv_extend, once per layer.  cu [B+1] int32 on the device does not
+ * decrease; rows outside all sequences are not read.  Rows without a valid
+ * slot, position or page are skipped (BITNET_ERR_PAGES).  A slot named twice
+ * gets the rows of one of the two.  Pages shared by several sequences are
+ * written as they are: bitnet_kv_fork shares full pages only, so appended
+ * rows never meet one.  The pages may not overlap each other, k or v.
+ */
+BITNET_API bitnet_status bitnet_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                          int64_t v_stride, const int32_t* cu,
+                                          const int32_t* slots, int64_t B, int64_t T, int64_t Hkv,
+                                          int64_t D, const bitnet_kv_tables* kv,
+                                          uint16_t* k_pages, uint16_t* v_pages, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache (the token's own key
+ * and value already appended): batch row b reads all lens[slot] tokens of slot
+ * slots[b] (NULL: b; a slot may be read by several rows).
+ * q, y [B, Hq, D] with row strides q_stride, y_stride; lse [B, Hq] or NULL.
+ * A slot or length outside the tables counts as empty, a page outside the
+ * pool as keys that are not seen (BITNET_ERR_PAGES).
+ * workspace  >= bitnet_attn_decode_workspace_size(B, Hq, Hkv, D) bytes.
+ * 1 <= B <= 65536.  y may not overlap q or the pages.
+ */
+BITNET_API size_t bitnet_attn_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv,
+                                                    int64_t D);
+BITNET_API bitnet_status bitnet_attn_decode(const uint16_t* q, int64_t q_stride,
+                                            const uint16_t* k_pages, const uint16_t* v_pages,
+                                            const bitnet_kv_tables* kv, const int32_t* slots,
+                                            int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                            float scale, uint16_t* y, int64_t y_stride,
+                                            float* lse, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * Fork: slot children[i] becomes a copy of slot parents[i].  Full pages are
+ * shared (their counts grow); a page that the parent fills in part gets a
+ * fresh page for the child, and the copy to make in every layer is listed.
+ * pairs    [n, 2] int32, written with (source, destination) of each copy;
+ * n_pairs  one int32, their number (both on the device, for
+ *          bitnet_kv_copy_pages).
+ * short_pages  as bitnet_kv_extend.  All or nothing.  Bad arguments are a slot
+ * outside the tables, a child that holds tokens, is named twice or is also a
+ * parent.  A parent may be named many times.
+ */
+BITNET_API bitnet_status bitnet_kv_fork(const bitnet_kv_tables* kv, const int32_t* parents,
+                                        const int32_t* children, int64_t n, int32_t* pairs,
+                                        int32_t* n_pairs, int32_t* short_pages, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Free n slots: their entries become -1, their lengths 0, and every page's
+ * count drops by the entries that named it.  Empty slots and slots named
+ * twice are fine; slots outside the tables are skipped (BITNET_ERR_PAGES).
+ */
+BITNET_API bitnet_status bitnet_kv_free(const bitnet_kv_tables* kv, const int32_t* slots,
+                                        int64_t n, void* stream);
+
+/*
+ * Compact: with L pages in use, those with index >= L move to the free ones
+ * below L, both in order, so that pages 0 .. L-1 are in use afterwards.  Tables
+ * and counts are changed, the copies to make in every layer listed.
+ * pairs [n_pages / 2, 2] int32 and n_pairs as bitnet_kv_fork (at least one
+ * pair's room); live: one int32 on the device (L) or NULL.
+ */
+BITNET_API bitnet_status bitnet_kv_compact(const bitnet_kv_tables* kv, int32_t* pairs,
+                                           int32_t* n_pairs, int32_t* live, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * Copy pages inside the caches of L layers: for each of the first *n_pairs
+ * pairs (at most max_pairs are read) page pairs[i][0] to page pairs[i][1],
+ * keys and values.  k_pages, v_pages: HOST arrays of L device pointers, read
+ * during the call only; page_bytes = Hkv * page_size * D * 2, a multiple of
+ * 16.  No destination may be named twice or also be a source (lists from
+ * bitnet_kv_fork and bitnet_kv_compact never do).  Pairs outside the pool are
+ * skipped (BITNET_ERR_PAGES).
+ */
+BITNET_API bitnet_status bitnet_kv_copy_pages(int64_t L, uint16_t* const* k_pages,
+                                              uint16_t* const* v_pages, int64_t n_pages,
+                                              int64_t page_bytes, const int32_t* pairs,
+                                              const int32_t* n_pairs, int64_t max_pairs,
+                                              void* stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: BITNET_OK, BITNET_ERR_TIMEOUT (a bounded wait expired; the
- * affected outputs are unspecified) or BITNET_ERR_NONFINITE.  A failing
+ * affected outputs are unspecified), BITNET_ERR_NONFINITE, BITNET_ERR_PAGES or
+ * BITNET_ERR_INVALID_ARG (sequence bounds outside their arrays).  A failing
  * synchronisation returns BITNET_ERR_CUDA.
  */
 BITNET_API bitnet_status bitnet_last_device_status(void* stream);

@@ -11,6 +11,7 @@ tensors holding the bit patterns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -23,7 +24,7 @@ LIB_PATH = os.path.join(_HERE, "libbitnet_b200.so")
 STATUS = {
     0: "BITNET_OK", 1: "BITNET_ERR_INVALID_ARG", 2: "BITNET_ERR_SHAPE", 3: "BITNET_ERR_ALIGN",
     4: "BITNET_ERR_WORKSPACE", 5: "BITNET_ERR_UNSUPPORTED", 6: "BITNET_ERR_CUDA",
-    7: "BITNET_ERR_TIMEOUT", 8: "BITNET_ERR_NONFINITE",
+    7: "BITNET_ERR_TIMEOUT", 8: "BITNET_ERR_NONFINITE", 9: "BITNET_ERR_PAGES",
 }
 
 # name -> (restype, argtypes)
@@ -60,12 +61,30 @@ SIGNATURES = {
     "bitnet_ffn_tp_down": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "bitnet_ffn_tp_finish": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _F, _P, _P,
                                             _P]),
+    "bitnet_attn_prompt": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64,
+                                          _I64, _I64, _I64, _F, _P, _I64, _P, _P]),
+    "bitnet_attn_decode_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "bitnet_attn_decode": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _F,
+                                          _P, _I64, _P, _P, _SZ, _P]),
+    "bitnet_kv_workspace_size": (_SZ, [_I64, _I64]),
+    "bitnet_kv_extend": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "bitnet_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P,
+                                        _P, _P, _P]),
+    "bitnet_kv_fork": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "bitnet_kv_free": (ctypes.c_int, [_P, _P, _I64, _P]),
+    "bitnet_kv_compact": (ctypes.c_int, [_P, _P, _P, _P, _P, _SZ, _P]),
+    "bitnet_kv_copy_pages": (ctypes.c_int, [_I64, _P, _P, _I64, _I64, _P, _P, _I64, _P]),
 }
 
 
 class FfnDebug(ctypes.Structure):
     _fields_ = [("xq1", _P), ("acc_gate", _P), ("acc_up", _P), ("h", _P), ("xq2", _P),
                 ("acc_down", _P), ("y_f32", _P)]
+
+
+class KvTables(ctypes.Structure):
+    _fields_ = [("table", _P), ("lens", _P), ("refs", _P), ("n_slots", _I64), ("max_pages", _I64),
+                ("n_pages", _I64), ("page_size", _I64)]
 
 
 class BitnetError(RuntimeError):
@@ -558,6 +577,261 @@ def bitnet_ffn_tp_finish(acc, I, gamma_down, amax2, sumsq_x, sumsq_h, eps=1e-5, 
                                     _stream())
     _check("bitnet_ffn_tp_finish", st)
     return y, y32
+
+
+# ------------------------------------------------- attention and its cache
+def _on(t):
+    """(context of) the device of t, for tensors that are not on the current one."""
+    d = t.device.index
+    return _HERE_CTX if d == torch.cuda.current_device() else torch.cuda.device(d)
+
+
+_HERE_CTX = contextlib.nullcontext()
+
+
+def _heads(t, name, device):
+    """A [tokens, heads, D] bf16 tensor on `device`, heads contiguous, any token stride."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dim() != 3 or t.element_size() != 2:
+        raise ValueError(f"{name} must be [tokens, heads, D] with 16-bit (bf16) elements")
+    n, h, d = t.shape
+    st = t.stride()
+    if n < 1 or (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
+        raise ValueError(f"{name} must have contiguous heads and at least one token")
+    return st[0] if n > 1 else max(st[0], h * d)
+
+
+def _pages(t, name, pool, device):
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.element_size() != 2 or t.dim() != 4 or t.shape[0] != pool.n_pages or \
+            t.shape[2] != pool.page_size:
+        raise ValueError(f"{name} must be [n_pages, heads, page_size, D] with 16-bit elements")
+    return t
+
+
+def _index(t, name, device, n=None):
+    """An int32 vector on `device` (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.dim() != 1:
+        raise ValueError(f"{name} must be a contiguous int32 vector on {device}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return t
+
+
+def _out(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.device != device or tuple(t.shape) != tuple(shape) or \
+            t.element_size() != torch.empty((), dtype=dtype).element_size():
+        raise ValueError(f"{name} must have shape {list(shape)} on {device}")
+    return t
+
+
+def bitnet_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                       cu_k=None, scale=None, y=None, want_lse: bool = False, lse=None):
+    """Causal attention over packed prompts: q [Tq,Hq,D], k and v [Tk,Hkv,D] bf16, sequence i in
+    rows cu_q[i] .. cu_q[i+1] and keys cu_k[i] .. (None: cu_q).  scale defaults to D ** -0.5.
+    Rows outside all sequences are left as they are.  Returns (y [Tq,Hq,D], lse [Tq,Hq] or None)."""
+    dev = q.device
+    qs, ks, vs = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or v.shape != k.shape:
+        raise ValueError("k and v must be [Tk, Hkv, D] with q's D")
+    _index(cu_q, "cu_q", dev)
+    cu_k = cu_q if cu_k is None else _index(cu_k, "cu_k", dev, cu_q.numel())
+    y = _out(y, "y", (Tq, Hq, D), torch.bfloat16, dev)
+    ys = _heads(y, "y", dev)
+    if want_lse or lse is not None:
+        lse = _dev(_out(lse, "lse", (Tq, Hq), torch.float32, dev), "lse")
+    with _on(q):
+        st = lib().bitnet_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                      cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1, Tq, Tk,
+                                      Hq, Hkv, D, D ** -0.5 if scale is None else scale,
+                                      y.data_ptr(), ys, _ptr(lse), _stream())
+    _check("bitnet_attn_prompt", st)
+    return y, lse
+
+
+class KvPool:
+    """Tables of a paged key-value cache (see bitnet_kv_tables): table
+    [n_slots, max_pages], lens [n_slots] and refs [n_pages], int32, in one
+    allocation.  Built empty by bitnet_kv_pool."""
+
+    def __init__(self, buf, n_slots, max_pages, n_pages, page_size, ws=None):
+        self.buf, self.page_size, self.ws = buf, page_size, ws
+        self.n_slots, self.max_pages, self.n_pages = n_slots, max_pages, n_pages
+        a, b = n_slots * max_pages, n_slots * max_pages + n_slots
+        self.table, self.lens, self.refs = buf[:a].view(n_slots, max_pages), buf[a:b], buf[b:]
+        p = buf.data_ptr()
+        self.c = KvTables(p, p + 4 * a, p + 4 * b, n_slots, max_pages, n_pages, page_size)
+        self.ref = ctypes.byref(self.c)
+
+    def clone(self):
+        """A copy of the tables (the pages are not part of a pool).  The copy shares the
+        scratch: use both on one stream."""
+        return KvPool(self.buf.clone(), self.n_slots, self.max_pages, self.n_pages,
+                      self.page_size, self.ws)
+
+
+def bitnet_kv_workspace_size(n_slots: int, n_pages: int) -> int:
+    return lib().bitnet_kv_workspace_size(n_slots, n_pages)
+
+
+def bitnet_kv_pool(n_slots: int, max_pages: int, n_pages: int, page_size: int,
+                   device="cuda") -> KvPool:
+    """An empty pool with its scratch.  Each layer's pages are [n_pages, Hkv, page_size, D]
+    tensors of the caller."""
+    nb = lib().bitnet_kv_workspace_size(n_slots, n_pages)
+    if nb == 0 or max_pages < 1:
+        raise ValueError("n_slots, max_pages or n_pages out of range")
+    buf = torch.empty(n_slots * max_pages + n_slots + n_pages, dtype=torch.int32, device=device)
+    if not buf.is_cuda:
+        raise ValueError("device must be a CUDA device")
+    pool = KvPool(buf, n_slots, max_pages, n_pages, page_size,
+                  torch.empty(nb, dtype=torch.uint8, device=device))
+    pool.table.fill_(-1)
+    pool.lens.zero_()
+    pool.refs.zero_()
+    return pool
+
+
+def bitnet_kv_extend(pool: KvPool, add: torch.Tensor, slots=None, short_pages=None):
+    """Sequences (slots, or 0, 1, ...) grow by add[i] tokens.  short_pages (optional int32 [1])
+    receives 0, the lacking pages or -1."""
+    dev = pool.buf.device
+    _index(add, "add", dev)
+    _index(slots, "slots", dev, add.numel())
+    _index(short_pages, "short_pages", dev, 1)
+    with _on(pool.buf):
+        st = lib().bitnet_kv_extend(pool.ref, _ptr(slots), add.data_ptr(), add.numel(),
+                                    _ptr(short_pages), pool.ws.data_ptr(), pool.ws.numel(),
+                                    _stream())
+    _check("bitnet_kv_extend", st)
+
+
+def bitnet_kv_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, pool: KvPool,
+                     k_pages: torch.Tensor, v_pages: torch.Tensor, slots=None):
+    """Rows cu[b] .. cu[b+1] of k and v [T,Hkv,D] become the last tokens of slot b (slots[b])."""
+    dev = pool.buf.device
+    ks, vs = _heads(k, "k", dev), _heads(v, "v", dev)
+    T, Hkv, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if _pages(t, name, pool, dev).shape[1] != Hkv or t.shape[3] != D:
+            raise ValueError(f"{name} must have k's heads and D")
+    _index(cu, "cu", dev)
+    _index(slots, "slots", dev, cu.numel() - 1)
+    with _on(pool.buf):
+        st = lib().bitnet_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, cu.data_ptr(), _ptr(slots),
+                                    cu.numel() - 1, T, Hkv, D, pool.ref, k_pages.data_ptr(),
+                                    v_pages.data_ptr(), _stream())
+    _check("bitnet_kv_append", st)
+
+
+def bitnet_attn_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return lib().bitnet_attn_decode_workspace_size(B, Hq, Hkv, D)
+
+
+def bitnet_attn_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pool: KvPool,
+                       slots=None, scale=None, y=None, want_lse: bool = False, lse=None,
+                       workspace=None):
+    """One new token per sequence over the paged cache: q [B,Hq,D], row b reads slot b (slots[b]).
+    Returns (y [B,Hq,D], lse [B,Hq] or None)."""
+    dev = pool.buf.device
+    qs = _heads(q, "q", dev)
+    B, Hq, D = q.shape
+    if _pages(k_pages, "k_pages", pool, dev).shape != _pages(v_pages, "v_pages", pool, dev).shape \
+            or k_pages.shape[3] != D:
+        raise ValueError("k_pages and v_pages must have one shape with q's D")
+    Hkv = k_pages.shape[1]
+    _index(slots, "slots", dev, B)
+    y = _out(y, "y", (B, Hq, D), torch.bfloat16, dev)
+    ys = _heads(y, "y", dev)
+    if want_lse or lse is not None:
+        lse = _dev(_out(lse, "lse", (B, Hq), torch.float32, dev), "lse")
+    nb = lib().bitnet_attn_decode_workspace_size(B, Hq, Hkv, D)
+    ws = _workspace(nb, dev, workspace)
+    with _on(q):
+        st = lib().bitnet_attn_decode(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
+                                      pool.ref, _ptr(slots), B, Hq, Hkv, D,
+                                      D ** -0.5 if scale is None else scale, y.data_ptr(), ys,
+                                      _ptr(lse), _ptr(ws), nb, _stream())
+    _check("bitnet_attn_decode", st)
+    return y, lse
+
+
+def bitnet_kv_fork(pool: KvPool, parents: torch.Tensor, children: torch.Tensor, short_pages=None,
+                   pairs=None, n_pairs=None):
+    """Slots children[i] become copies of parents[i].  Returns (pairs [n,2], n_pairs [1]): the page
+    copies that bitnet_kv_copy_pages has to make in every layer."""
+    dev = pool.buf.device
+    _index(parents, "parents", dev)
+    n = parents.numel()
+    _index(children, "children", dev, n)
+    _index(short_pages, "short_pages", dev, 1)
+    pairs = _dev(_out(pairs, "pairs", (n, 2), torch.int32, dev), "pairs")
+    n_pairs = _out(n_pairs, "n_pairs", (1,), torch.int32, dev)
+    with _on(pool.buf):
+        st = lib().bitnet_kv_fork(pool.ref, parents.data_ptr(), children.data_ptr(), n,
+                                  pairs.data_ptr(), n_pairs.data_ptr(), _ptr(short_pages),
+                                  pool.ws.data_ptr(), pool.ws.numel(), _stream())
+    _check("bitnet_kv_fork", st)
+    return pairs, n_pairs
+
+
+def bitnet_kv_free(pool: KvPool, slots: torch.Tensor):
+    """Free slots: their pages' counts drop, their rows become empty."""
+    _index(slots, "slots", pool.buf.device)
+    with _on(pool.buf):
+        st = lib().bitnet_kv_free(pool.ref, slots.data_ptr(), slots.numel(), _stream())
+    _check("bitnet_kv_free", st)
+
+
+def bitnet_kv_compact(pool: KvPool, live=None, pairs=None, n_pairs=None):
+    """Move the pages in use to the front of the pool.  Returns (pairs, n_pairs) for
+    bitnet_kv_copy_pages; live (optional int32 [1]) receives the number of pages in use."""
+    dev = pool.buf.device
+    _index(live, "live", dev, 1)
+    shape = (max(1, pool.n_pages // 2), 2)
+    pairs = _dev(_out(pairs, "pairs", shape, torch.int32, dev), "pairs")
+    n_pairs = _out(n_pairs, "n_pairs", (1,), torch.int32, dev)
+    with _on(pool.buf):
+        st = lib().bitnet_kv_compact(pool.ref, pairs.data_ptr(), n_pairs.data_ptr(), _ptr(live),
+                                     pool.ws.data_ptr(), pool.ws.numel(), _stream())
+    _check("bitnet_kv_compact", st)
+    return pairs, n_pairs
+
+
+def bitnet_kv_copy_pages(k_pages, v_pages, pairs: torch.Tensor, n_pairs: torch.Tensor):
+    """Make the listed page copies in every layer: k_pages, v_pages are lists of the layers'
+    [n_pages, Hkv, page_size, D] tensors, all of one shape."""
+    if len(k_pages) != len(v_pages) or not k_pages:
+        raise ValueError("k_pages and v_pages must be non-empty lists of equal length")
+    first = k_pages[0]
+    dev, shape = first.device, first.shape
+    L = len(k_pages)
+    for t in (*k_pages, *v_pages):
+        if t.shape != shape or t.device != dev or t.element_size() != 2 or not t.is_cuda or \
+                not t.is_contiguous():
+            raise ValueError("all pages must be contiguous 16-bit CUDA tensors of one shape")
+    _index(n_pairs, "n_pairs", dev, 1)
+    if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or \
+            pairs.device != dev or not pairs.is_contiguous():
+        raise ValueError("pairs must be a contiguous [n, 2] int32 tensor")
+    K = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_pages])
+    V = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_pages])
+    page_bytes = first[0].numel() * 2
+    with _on(first):
+        st = lib().bitnet_kv_copy_pages(L, K, V, shape[0], page_bytes, pairs.data_ptr(),
+                                        n_pairs.data_ptr(), min(pairs.shape[0], shape[0]),
+                                        _stream())
+    _check("bitnet_kv_copy_pages", st)
 
 
 def bitnet_last_device_status() -> int:

@@ -10,7 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbitnet_b200.so")
 SOURCES = ["bitnet_all.cu", "common.cuh", "pack.cu", "quant.cu", "gemv.cu", "resident.cu", "batched.cu", "gemm.cu", "a48.cu", "api.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "attention.cuh", "attn_prompt.cu", "attn_decode.cu", "kvcache.cu",
+           "attention_api.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

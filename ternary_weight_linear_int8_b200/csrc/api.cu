@@ -329,6 +329,7 @@ const char* bitnet_status_string(int status) {
     case BITNET_ERR_CUDA: return "BITNET_ERR_CUDA";
     case BITNET_ERR_TIMEOUT: return "BITNET_ERR_TIMEOUT";
     case BITNET_ERR_NONFINITE: return "BITNET_ERR_NONFINITE";
+    case BITNET_ERR_PAGES: return "BITNET_ERR_PAGES";
     default: return "BITNET_ERR_UNKNOWN";
   }
 }

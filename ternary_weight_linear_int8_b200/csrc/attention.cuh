@@ -1,0 +1,107 @@
+// Helpers shared by the attention and key-value cache kernels: warp-level bf16
+// matrix instructions and their shared-memory loads, 16-byte asynchronous
+// copies, exponentials, the paged cache's addressing and a block scan.
+#pragma once
+
+#include "common.cuh"
+
+namespace bitnet {
+
+// Page tables of a cache (one set of tables for all layers).
+struct KvTables {
+  int32_t* table;       // [n_slots, max_pages] page of each entry, -1 where none
+  int32_t* lens;        // [n_slots] tokens held
+  int32_t* refs;        // [n_pages] table entries that name the page (0: free)
+  int n_slots, max_pages, n_pages, page_size;
+};
+
+// ----------------------------------------------------------- warp matrices
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// c[16x8] += a[16x16] b[16x8], bf16 operands, fp32 sums
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two fp32 values as a bf16 pair, round to nearest even (lo in the low half)
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------ asynchronous copies
+// 16 bytes global -> shared; with `bytes` = 0 the destination is zeroed and
+// nothing is read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2^x by the hardware's approximation (2 ulp; 0 for -inf)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Address of 16-byte chunk c of row r in a shared tile of D-wide bf16 rows:
+// the chunk index is xored with the row so that eight rows of one logical
+// chunk (what ldmatrix reads) lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c) {
+  return base + (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+// Exclusive sum over the block's threads (at most 1024), with the total.
+// `red` holds 33 ints.
+__device__ __forceinline__ int block_exclusive_sum(int v, int* red, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();                 // the previous call's values are read
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < nw ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += t;
+    }
+    red[lane] = w;                 // inclusive sums of the warps
+  }
+  __syncthreads();
+  total = red[nw - 1];
+  return inc - v + (warp ? red[warp - 1] : 0);
+}
+
+}  // namespace bitnet

@@ -1,0 +1,368 @@
+// C ABI of the attention and key-value cache operators: argument validation
+// and launches.  Contracts are in include/bitnet.h.
+#include <cmath>
+
+#include "attention.cuh"
+
+using namespace bitnet;
+
+namespace {
+
+constexpr int64_t kMaxI32 = 0x7fffffff;
+constexpr double kLog2e = 1.4426950408889634;
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool ranges_overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// Launch with programmatic dependent launch (every kernel here begins with
+// griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                       cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// The checks every call with tables shares.
+bitnet_status check_tables(const bitnet_kv_tables* kv) {
+  if (!kv || !kv->table || !kv->lens || !kv->refs) return BITNET_ERR_INVALID_ARG;
+  if (kv->n_slots < 1 || kv->n_slots > kKvMaxSlots || kv->max_pages < 1 || kv->n_pages < 1 ||
+      kv->n_pages > (1 << 30) || kv->page_size < 16 || kv->page_size > 1024 ||
+      kv->page_size % 16 != 0 || kv->max_pages > kMaxI32 / 2 / kv->page_size)
+    return BITNET_ERR_SHAPE;
+  if (!aligned4(kv->table) || !aligned4(kv->lens) || !aligned4(kv->refs)) return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+KvTables device_tables(const bitnet_kv_tables* kv) {
+  KvTables t{};
+  t.table = kv->table;
+  t.lens = kv->lens;
+  t.refs = kv->refs;
+  t.n_slots = (int)kv->n_slots;
+  t.max_pages = (int)kv->max_pages;
+  t.n_pages = (int)kv->n_pages;
+  t.page_size = (int)kv->page_size;
+  return t;
+}
+
+bool heads_ok(int64_t Hq, int64_t Hkv, int64_t D) {
+  return (D == 64 || D == 128) && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 &&
+         Hq / Hkv <= 64;
+}
+bool stride_ok(int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 && stride <= kMaxI32;
+}
+
+// The decode kernel's workspace: partial outputs, their maxima and sums, the
+// first unit of every row.
+struct DecodeWs {
+  int hb, rows;
+  size_t part, ml, first, total;
+};
+DecodeWs decode_ws(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  DecodeWs w{};
+  const int g = (int)(Hq / Hkv);
+  w.hb = (g + 15) / 16;
+  w.rows = (g + w.hb - 1) / w.hb;
+  const size_t n = (size_t)2 * kDecMaxCtas * w.rows;
+  w.part = 0;
+  w.ml = al256(n * D * 4);
+  w.first = w.ml + al256(n * 8);
+  w.total = w.first + al256((size_t)(B + 1) * 8);
+  return w;
+}
+
+template <int D, int NT>
+bitnet_status decode_launch(const AttnDecodeArgs& a, int ctas, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  constexpr int smem = dec_smem_bytes<D, NT>();
+  if (set_smem_attr_once(configured, attn_decode_kernel<D, NT>, smem) != cudaSuccess)
+    return BITNET_ERR_CUDA;
+  if (launch_pdl(attn_decode_kernel<D, NT>, (unsigned)ctas, kDecWarps * 32, smem, s, a) !=
+      cudaSuccess)
+    return BITNET_ERR_CUDA;
+  const int64_t blocks = ((int64_t)a.B * a.Hq + 3) / 4;
+  if (launch_pdl(attn_join_kernel<D>, (unsigned)blocks, 128, 0, s, a, ctas) != cudaSuccess)
+    return BITNET_ERR_CUDA;
+  return BITNET_OK;
+}
+
+template <int D>
+bitnet_status prompt_warp_launch(AttnPromptArgs a, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  constexpr int smem = pw_smem_bytes<D>();
+  if (set_smem_attr_once(configured, prompt_warp_kernel<D>, smem) != cudaSuccess)
+    return BITNET_ERR_CUDA;
+  a.tile_tokens = kPwRows / a.group;
+  const int64_t grid = ((int64_t)(a.Tq / a.tile_tokens) + a.B) * a.Hkv;
+  if (grid > kMaxI32) return BITNET_ERR_SHAPE;
+  return launch_pdl(prompt_warp_kernel<D>, (unsigned)grid, 128, smem, s, a) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+unsigned kv_blocks(int64_t items, int num_sms) {
+  const int64_t b = (items + 255) / 256;
+  return (unsigned)(b < (int64_t)num_sms * 8 ? b : (int64_t)num_sms * 8);
+}
+
+}  // namespace
+
+extern "C" {
+
+bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                 int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                 const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
+                                 int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale,
+                                 uint16_t* y, int64_t y_stride, float* lse, void* stream) {
+  if (!q || !k || !v || !cu_q || !cu_k || !y) return BITNET_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return BITNET_ERR_INVALID_ARG;
+  if (B < 1 || B > kMaxI32 / 2 || Tq < 1 || Tq > kMaxI32 / 2 || Tk < 1 || Tk > kMaxI32 / 2 ||
+      !heads_ok(Hq, Hkv, D) || !stride_ok(q_stride, Hq * D) || !stride_ok(y_stride, Hq * D) ||
+      !stride_ok(k_stride, Hkv * D) || !stride_ok(v_stride, Hkv * D))
+    return BITNET_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(y) || !aligned4(cu_q) ||
+      !aligned4(cu_k) || !aligned4(lse))
+    return BITNET_ERR_ALIGN;
+  const int64_t yb = ((Tq - 1) * y_stride + Hq * D) * 2;
+  if (ranges_overlap(y, yb, q, ((Tq - 1) * q_stride + Hq * D) * 2) ||
+      ranges_overlap(y, yb, k, ((Tk - 1) * k_stride + Hkv * D) * 2) ||
+      ranges_overlap(y, yb, v, ((Tk - 1) * v_stride + Hkv * D) * 2))
+    return BITNET_ERR_INVALID_ARG;
+  DevInfo d;
+  const bitnet_status st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  AttnPromptArgs a{};
+  a.q = q; a.k = k; a.v = v;
+  a.cu_q = cu_q; a.cu_k = cu_k;
+  a.y = y; a.lse = lse;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.y_stride = y_stride;
+  a.B = (int)B; a.Tq = (int)Tq; a.Tk = (int)Tk;
+  a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.group = (int)(Hq / Hkv);
+  a.scale_log2 = (float)((double)scale * kLog2e);
+  return D == 64 ? prompt_warp_launch<64>(a, as_stream(stream))
+                 : prompt_warp_launch<128>(a, as_stream(stream));
+}
+
+size_t bitnet_attn_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (B < 1 || B > kKvMaxSlots || !heads_ok(Hq, Hkv, D)) return 0;
+  return decode_ws(B, Hq, Hkv, D).total;
+}
+
+bitnet_status bitnet_attn_decode(const uint16_t* q, int64_t q_stride, const uint16_t* k_pages,
+                                 const uint16_t* v_pages, const bitnet_kv_tables* kv,
+                                 const int32_t* slots, int64_t B, int64_t Hq, int64_t Hkv,
+                                 int64_t D, float scale, uint16_t* y, int64_t y_stride,
+                                 float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (!q || !k_pages || !v_pages || !y) return BITNET_ERR_INVALID_ARG;
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return BITNET_ERR_INVALID_ARG;
+  if (B < 1 || B > kKvMaxSlots || (!slots && B > kv->n_slots) || !heads_ok(Hq, Hkv, D) ||
+      !stride_ok(q_stride, Hq * D) || !stride_ok(y_stride, Hq * D))
+    return BITNET_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(y) ||
+      !aligned4(slots) || !aligned4(lse))
+    return BITNET_ERR_ALIGN;
+  const int64_t yb = ((B - 1) * y_stride + Hq * D) * 2;
+  const int64_t cb = kv->n_pages * Hkv * kv->page_size * D * 2;
+  if (ranges_overlap(y, yb, q, ((B - 1) * q_stride + Hq * D) * 2) ||
+      ranges_overlap(y, yb, k_pages, cb) || ranges_overlap(y, yb, v_pages, cb))
+    return BITNET_ERR_INVALID_ARG;
+  const DecodeWs w = decode_ws(B, Hq, Hkv, D);
+  if (!workspace || workspace_bytes < w.total) return BITNET_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  AttnDecodeArgs a{};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = q; a.k_pages = k_pages; a.v_pages = v_pages;
+  a.kv = device_tables(kv);
+  a.slots = slots;
+  a.y = y; a.lse = lse;
+  a.q_stride = q_stride; a.y_stride = y_stride;
+  a.B = (int)B; a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.group = (int)(Hq / Hkv);
+  a.hb = w.hb; a.rows = w.rows;
+  a.scale_log2 = (float)((double)scale * kLog2e);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  a.first_unit = reinterpret_cast<int64_t*>(ws + w.first);
+  const int ctas = 2 * d.num_sms < kDecMaxCtas ? 2 * d.num_sms : kDecMaxCtas;
+  cudaStream_t s = as_stream(stream);
+  if (D == 64) return w.rows <= 8 ? decode_launch<64, 1>(a, ctas, s) : decode_launch<64, 2>(a, ctas, s);
+  return w.rows <= 8 ? decode_launch<128, 1>(a, ctas, s) : decode_launch<128, 2>(a, ctas, s);
+}
+
+size_t bitnet_kv_workspace_size(int64_t n_slots, int64_t n_pages) {
+  if (n_slots < 1 || n_slots > kKvMaxSlots || n_pages < 1 || n_pages > (1 << 30)) return 0;
+  return al256((size_t)(4 + n_slots + 2 * n_pages) * 4);
+}
+
+bitnet_status bitnet_kv_extend(const bitnet_kv_tables* kv, const int32_t* slots,
+                               const int32_t* add, int64_t n, int32_t* short_pages,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (!add) return BITNET_ERR_INVALID_ARG;
+  if (n < 1 || n > kv->n_slots) return BITNET_ERR_SHAPE;
+  if (!aligned4(slots) || !aligned4(add) || !aligned4(short_pages)) return BITNET_ERR_ALIGN;
+  if (!workspace || workspace_bytes < bitnet_kv_workspace_size(kv->n_slots, kv->n_pages))
+    return BITNET_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  return launch_pdl(kv_extend_kernel, 1, kKvThreads, 0, as_stream(stream), device_tables(kv), slots,
+                    add, (int)n, short_pages, static_cast<int32_t*>(workspace)) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+bitnet_status bitnet_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                               int64_t v_stride, const int32_t* cu, const int32_t* slots,
+                               int64_t B, int64_t T, int64_t Hkv, int64_t D,
+                               const bitnet_kv_tables* kv, uint16_t* k_pages, uint16_t* v_pages,
+                               void* stream) {
+  if (!k || !v || !cu || !k_pages || !v_pages) return BITNET_ERR_INVALID_ARG;
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (B < 1 || B > kKvMaxSlots || (!slots && B > kv->n_slots) || T < 1 || T > kMaxI32 / 2 ||
+      !heads_ok(Hkv, Hkv, D) || !stride_ok(k_stride, Hkv * D) || !stride_ok(v_stride, Hkv * D))
+    return BITNET_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned4(cu) || !aligned4(slots))
+    return BITNET_ERR_ALIGN;
+  const int64_t cb = kv->n_pages * Hkv * kv->page_size * D * 2;
+  const int64_t kb = ((T - 1) * k_stride + Hkv * D) * 2, vb = ((T - 1) * v_stride + Hkv * D) * 2;
+  if (ranges_overlap(k_pages, cb, v_pages, cb) || ranges_overlap(k_pages, cb, k, kb) ||
+      ranges_overlap(k_pages, cb, v, vb) || ranges_overlap(v_pages, cb, k, kb) ||
+      ranges_overlap(v_pages, cb, v, vb))
+    return BITNET_ERR_INVALID_ARG;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  KvAppendArgs a{};
+  a.k = k; a.v = v; a.cu = cu; a.slots = slots;
+  a.kv = device_tables(kv);
+  a.k_pages = k_pages; a.v_pages = v_pages;
+  a.k_stride = k_stride; a.v_stride = v_stride;
+  a.B = (int)B; a.T = (int)T; a.Hkv = (int)Hkv; a.head_chunks = (int)(D / 8);
+  return launch_pdl(kv_append_kernel, (unsigned)((T + 7) / 8), 256, 0, as_stream(stream), a) ==
+                 cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+bitnet_status bitnet_kv_fork(const bitnet_kv_tables* kv, const int32_t* parents,
+                             const int32_t* children, int64_t n, int32_t* pairs, int32_t* n_pairs,
+                             int32_t* short_pages, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (!parents || !children || !pairs || !n_pairs) return BITNET_ERR_INVALID_ARG;
+  if (n < 1 || n > kv->n_slots) return BITNET_ERR_SHAPE;
+  if (!aligned4(parents) || !aligned4(children) || !aligned4(pairs) || !aligned4(n_pairs) ||
+      !aligned4(short_pages))
+    return BITNET_ERR_ALIGN;
+  if (!workspace || workspace_bytes < bitnet_kv_workspace_size(kv->n_slots, kv->n_pages))
+    return BITNET_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  const KvTables t = device_tables(kv);
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  cudaStream_t s = as_stream(stream);
+  if (launch_pdl(kv_fork_plan_kernel, 1, kKvThreads, 0, s, t, parents, children, (int)n, pairs,
+                 n_pairs, short_pages, ws) != cudaSuccess)
+    return BITNET_ERR_CUDA;
+  return launch_pdl(kv_fork_rows_kernel, kv_blocks(n * kv->max_pages, d.num_sms), 256, 0, s, t,
+                    parents, children, (int)n, (const int32_t*)ws) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+bitnet_status bitnet_kv_free(const bitnet_kv_tables* kv, const int32_t* slots, int64_t n,
+                             void* stream) {
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (!slots) return BITNET_ERR_INVALID_ARG;
+  if (n < 1 || n > kKvMaxSlots) return BITNET_ERR_SHAPE;
+  if (!aligned4(slots)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  return launch_pdl(kv_free_kernel, kv_blocks(n * kv->max_pages, d.num_sms), 256, 0,
+                    as_stream(stream), device_tables(kv), slots, (int)n) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+bitnet_status bitnet_kv_compact(const bitnet_kv_tables* kv, int32_t* pairs, int32_t* n_pairs,
+                                int32_t* live, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  bitnet_status st = check_tables(kv);
+  if (st != BITNET_OK) return st;
+  if (!pairs || !n_pairs) return BITNET_ERR_INVALID_ARG;
+  if (!aligned4(pairs) || !aligned4(n_pairs) || !aligned4(live)) return BITNET_ERR_ALIGN;
+  if (!workspace || workspace_bytes < bitnet_kv_workspace_size(kv->n_slots, kv->n_pages))
+    return BITNET_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  const KvTables t = device_tables(kv);
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  cudaStream_t s = as_stream(stream);
+  if (launch_pdl(kv_compact_plan_kernel, 1, kKvThreads, 0, s, t, pairs, n_pairs, live, ws) !=
+      cudaSuccess)
+    return BITNET_ERR_CUDA;
+  return launch_pdl(kv_compact_table_kernel, kv_blocks(kv->n_slots * kv->max_pages, d.num_sms), 256,
+                    0, s, t, (const int32_t*)ws) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+bitnet_status bitnet_kv_copy_pages(int64_t L, uint16_t* const* k_pages, uint16_t* const* v_pages,
+                                   int64_t n_pages, int64_t page_bytes, const int32_t* pairs,
+                                   const int32_t* n_pairs, int64_t max_pairs, void* stream) {
+  if (!k_pages || !v_pages || !pairs || !n_pairs || L < 1) return BITNET_ERR_INVALID_ARG;
+  if (n_pages < 1 || n_pages > (1 << 30) || page_bytes < 16 || page_bytes % 16 != 0 ||
+      page_bytes > (int64_t(1) << 34) || max_pairs < 1 || max_pairs > n_pages || L > 65536)
+    return BITNET_ERR_SHAPE;
+  for (int64_t l = 0; l < L; ++l) {
+    if (!k_pages[l] || !v_pages[l]) return BITNET_ERR_INVALID_ARG;
+    if (!aligned16(k_pages[l]) || !aligned16(v_pages[l])) return BITNET_ERR_ALIGN;
+  }
+  if (!aligned4(pairs) || !aligned4(n_pairs)) return BITNET_ERR_ALIGN;
+  DevInfo d;
+  const bitnet_status st = device_info(&d);
+  if (st != BITNET_OK) return st;
+  for (int64_t l0 = 0; l0 < L; l0 += kCopyLayers) {
+    const int layers = (int)(L - l0 < kCopyLayers ? L - l0 : kCopyLayers);
+    KvCopyArgs a{};
+    for (int l = 0; l < layers; ++l) {
+      a.base[2 * l] = reinterpret_cast<uint4*>(k_pages[l0 + l]);
+      a.base[2 * l + 1] = reinterpret_cast<uint4*>(v_pages[l0 + l]);
+    }
+    a.pairs = pairs; a.n_pairs = n_pairs;
+    a.max_pairs = (int)max_pairs; a.n_pages = (int)n_pages; a.planes = 2 * layers;
+    a.page_chunks = page_bytes / 16;
+    if (launch_pdl(kv_copy_kernel, (unsigned)(d.num_sms * 8), kCopyThreads, 0, as_stream(stream),
+                   a) != cudaSuccess)
+      return BITNET_ERR_CUDA;
+  }
+  return BITNET_OK;
+}
+
+}  // extern "C"
