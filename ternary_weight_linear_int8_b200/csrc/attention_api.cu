@@ -101,6 +101,11 @@ bitnet_status decode_launch(const AttnDecodeArgs& a, int ctas, cudaStream_t s) {
   return BITNET_OK;
 }
 
+// Upper bound of the tiles of `tokens` tokens (the lengths are on the device).
+int64_t prompt_ctas(const AttnPromptArgs& a, int tokens) {
+  return ((int64_t)(a.Tq / tokens) + a.B) * a.Hkv;
+}
+
 template <int D>
 bitnet_status prompt_warp_launch(AttnPromptArgs a, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
@@ -108,9 +113,53 @@ bitnet_status prompt_warp_launch(AttnPromptArgs a, cudaStream_t s) {
   if (set_smem_attr_once(configured, prompt_warp_kernel<D>, smem) != cudaSuccess)
     return BITNET_ERR_CUDA;
   a.tile_tokens = kPwRows / a.group;
-  const int64_t grid = ((int64_t)(a.Tq / a.tile_tokens) + a.B) * a.Hkv;
+  const int64_t grid = prompt_ctas(a, a.tile_tokens);
   if (grid > kMaxI32) return BITNET_ERR_SHAPE;
   return launch_pdl(prompt_warp_kernel<D>, (unsigned)grid, 128, smem, s, a) == cudaSuccess
+             ? BITNET_OK : BITNET_ERR_CUDA;
+}
+
+// Tokens by heads by D: a map whose boxes are 64 columns of `heads` heads of
+// `tokens` tokens, 128-byte swizzled.
+bool make_map_tokens(CUtensorMap* m, const void* base, int64_t D, int64_t H, int64_t T,
+                     int64_t stride, uint32_t heads, uint32_t tokens) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, heads, tokens}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+bitnet_status prompt_tile_launch(AttnPromptArgs a, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  constexpr size_t smem = PtCfg<D>::kSmem;
+  if (set_smem_attr_once(configured, prompt_tile_kernel<D>, (int)smem) != cudaSuccess)
+    return BITNET_ERR_CUDA;
+  const int half = 128 / a.group;
+  a.half_tokens = half;
+  a.tile_tokens = 2 * half;
+  int64_t grid = prompt_ctas(a, a.tile_tokens);
+  // Too few tiles for the SMs: tiles of one half each, twice as many (a CTA's
+  // step is then bound by its own softmax and takes about 0.85 of the time of
+  // two halves).  512 tokens of 20 heads 16.1 -> 13.4 us, 1000 rows on 5000
+  // keys of 16 heads of 64 71 -> 60 us; but not where the halves need a
+  // second wave of short tiles (512 tokens of 64 heads: 17.8 -> 22.2 us).
+  if (grid <= num_sms && (prompt_ctas(a, half) <= num_sms || (int64_t)a.Tk >= 1024 * (int64_t)a.B)) {
+    a.tile_tokens = half;
+    grid = prompt_ctas(a, half);
+  }
+  if (grid > kMaxI32) return BITNET_ERR_SHAPE;
+  CUtensorMap tq, tk, tv;
+  if (!make_map_tokens(&tq, a.q, D, a.Hq, a.Tq, a.q_stride, (uint32_t)a.group, (uint32_t)half) ||
+      !make_map_tokens(&tk, a.k, D, a.Hkv, a.Tk, a.k_stride, 1, kPtKeys) ||
+      !make_map_tokens(&tv, a.v, D, a.Hkv, a.Tk, a.v_stride, 1, kPtKeys))
+    return BITNET_ERR_CUDA;
+  return launch_pdl(prompt_tile_kernel<D>, (unsigned)grid, kPtThreads, smem, s, tq, tk, tv, a) ==
+                 cudaSuccess
              ? BITNET_OK : BITNET_ERR_CUDA;
 }
 
@@ -153,8 +202,17 @@ bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint
   a.B = (int)B; a.Tq = (int)Tq; a.Tk = (int)Tk;
   a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.group = (int)(Hq / Hkv);
   a.scale_log2 = (float)((double)scale * kLog2e);
-  return D == 64 ? prompt_warp_launch<64>(a, as_stream(stream))
-                 : prompt_warp_launch<128>(a, as_stream(stream));
+  // Short prompts, few of them: the warp kernel starts faster (no tensor
+  // memory, no tensor maps; 4.1 against 7.5 us for one token).  With 20 heads of 128
+  // it takes 7.4 / 9.3 / 11.7 us for 128 / 200 / 300 tokens, the tile kernel
+  // 8.5 / 10.0 / 11.3, and beyond one wave of CTAs the tile kernel wins
+  // earlier (256 tokens of 64 heads: 14.5 against 10.2 us).
+  const bool few = prompt_ctas(a, kPwRows / a.group) * 2 <= 3 * d.num_sms && Tk <= 256 * B;
+  if (few)
+    return D == 64 ? prompt_warp_launch<64>(a, as_stream(stream))
+                   : prompt_warp_launch<128>(a, as_stream(stream));
+  return D == 64 ? prompt_tile_launch<64>(a, d.num_sms, as_stream(stream))
+                 : prompt_tile_launch<128>(a, d.num_sms, as_stream(stream));
 }
 
 size_t bitnet_attn_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {

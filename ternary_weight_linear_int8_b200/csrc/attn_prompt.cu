@@ -25,6 +25,7 @@ struct AttnPromptArgs {
   int64_t q_stride, k_stride, v_stride, y_stride;
   int B, Tq, Tk, Hq, Hkv, group;
   int tile_tokens;        // tokens per tile
+  int half_tokens;        // tile kernel: tokens per 128 rows
   float scale_log2;       // scale * log2(e)
 };
 
@@ -307,6 +308,563 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
     const int r = warp * 16 + (bit >> 2) + 8 * (bit & 3);
     __syncwarp();
     prompt_row_by_warp<D>(a, t, t.t0 + r / a.group, kvh * a.group + r % a.group);
+  }
+}
+
+
+// ------------------------------------------------------------ tensor cores
+//
+// The tile kernel: 2 x 128 rows per CTA on tcgen05.  Twenty warps:
+//   * 16 softmax warps, 8 for each 128 rows: a thread has one row (a TMEM
+//     lane) and half of a key tile's columns, so four of them share a
+//     scheduler and hide each other's latencies;
+//   * warp 16 (one thread): TMA loads of Q once and of K, V tiles of 128 keys
+//     into a ring;
+//   * warp 17 (one thread): the MMAs.
+// Per key tile j and row half i:
+//   S_i = Q_i K_j^T   both operands in shared memory, fp32 scores in TMEM
+//   P_i = exp2(c S_i - m_i)   read by the softmax threads, written back over
+//                             S_i as bf16 pairs (64 of its 128 columns)
+//   O_i += P_i V_j    P_i from TMEM, V_j (rows of D values, so MN-major) from
+//                     shared memory, fp32 sums in TMEM
+// The halves alternate: while one half's scores are in the softmax the tensor
+// cores run the other half's two products.  MMAs are executed in
+// issue order, so S_i of tile j + 1 may overwrite P_i as soon as it is issued
+// after O_i += P_i V_j, and its completion says that O_i is up to date.
+//
+// The reference m_i of a row only has to keep the exponentials in range, not
+// to be the running maximum: the result is divided by the same scaled sum.  So
+// a tile's exponentials are taken with the reference of the tiles before it
+// while its own maximum is still being found, and only if a row outgrows its
+// reference by 2^8 (always in the first tile) is the tile done again, with
+// O_i rescaled.  bf16 has fp32's range, so probabilities up to 2^8 lose
+// nothing.
+constexpr int kPtKeys = 128;
+constexpr int kPtThreads = 640;
+constexpr int kPtRegs = 96;                  // 65536 / 640, in steps of 8
+constexpr int kPtRegsSoftmax = 104, kPtRegsIssue = 64;
+static_assert(512 * kPtRegsSoftmax + 128 * kPtRegsIssue <= kPtThreads * kPtRegs,
+              "the warpgroups' registers come from the launch's");
+template <int D>
+struct PtCfg {
+  static constexpr int kHalves = D / 64;                  // 128-byte wide column blocks
+  static constexpr int kBlock = 128 * 128;                // 128 rows of 64 bf16
+  static constexpr int kTile = kHalves * kBlock;          // a Q half, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kBars = 2 * kStages + 8;
+  static constexpr int kExch = 2 * 2 * 128 * 4;           // a float per softmax thread
+  static constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + kExch + kBars * 8 + 64;
+  // D fp32, A and B bf16, M 128; scores: N 128, both K-major; outputs: N = D, B MN-major
+  static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) |
+                                      ((uint32_t)(kPtKeys >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                                      ((uint32_t)(D >> 3) << 17) | (8u << 24);
+};
+
+// Barrier of the two warps that share 32 rows; `any` tells whether the
+// condition holds in one of their threads.
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Shared-memory descriptor of an MN-major operand in 128-byte swizzled rows:
+// 64 columns per 128-byte row, the next 64 columns `block` bytes on, 8 rows
+// (of the contraction) per 1024 bytes.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3fffu);
+  d |= (uint64_t)(block >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+__device__ __forceinline__ void tc_mma_bf16(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t dtmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dtmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes; the registers are valid after
+// tcgen05.wait::ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// Waits for this thread's loads; the 32 registers pass through it, so no use
+// of them can be scheduled before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Two fp32 lanes in one 64-bit register pair.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// True in one lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+// The largest of three, NaN if one of them is NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of a pair on the fp32 pipe, for -inf <= x < 128: n = x rounded to an
+// integer (by adding 1.5 * 2^23), 2^(x - n) by a polynomial whose constant term
+// is 1 and whose other coefficients minimise the largest relative error on
+// [-1/2, 1/2] (weighted least squares with Lawson's weights; 1.1e-7, below
+// the hardware approximation's 2 ulp), n added to the exponent field.  x is
+// held at -127, where the field becomes 0: masked scores give exactly 0.
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  x = f2_pack(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  const uint64_t big = f2_pack(12582912.0f, 12582912.0f), neg = f2_pack(-12582912.0f, -12582912.0f);
+  const uint64_t t = f2_add(x, big), n = f2_add(t, neg);
+  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
+  uint64_t p = f2_fma(f, f2_pack(0.0013264727f, 0.0013264727f), f2_pack(0.009671513f, 0.009671513f));
+  p = f2_fma(p, f, f2_pack(0.055507336f, 0.055507336f));
+  p = f2_fma(p, f, f2_pack(0.24022242f, 0.24022242f));
+  p = f2_fma(p, f, f2_pack(0.693147f, 0.693147f));
+  p = f2_fma(p, f, f2_pack(1.0f, 1.0f));
+  float pa, pb, ta, tb;
+  f2_unpack(p, pa, pb);
+  f2_unpack(t, ta, tb);
+  return f2_pack(__int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23)),
+                 __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23)));
+}
+// Of every eight pairs of scores so many take ex2_pair, the others the special
+// function unit (4 exponentials per clock and scheduler, which alone would
+// take as long as the tensor cores' products).  4096-token prefill of 20 heads
+// with 0 / 2 / 3 / 4 of 8: 97.9 / 95.4 / 95.8 / 106 us; 16384 tokens: 1230 /
+// 1138 / 1186 / 1354.
+constexpr int kPtEmulated = 2;
+
+template <int D>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    prompt_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const AttnPromptArgs a) {
+  using C = PtCfg<D>;
+  constexpr int S = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];      // the swizzled tiles come first
+  uint8_t* ring = smem + 2 * C::kTile;
+  float* exch = reinterpret_cast<float*>(ring + (size_t)S * C::kTile);   // [2 halves][2][128]
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(exch + C::kExch / 4);
+  uint64_t* kv_empty = kv_full + S;
+  uint64_t* q_full = kv_empty + S;
+  uint64_t* s_full = q_full + 1;             // [2]
+  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* o_full = p_full + 2;             // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_full + C::kBars);
+  PromptTile* s_tile = reinterpret_cast<PromptTile*>(tmem_slot + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int kvh = blockIdx.x % a.Hkv;
+  if (tid == 512) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);
+      mbar_init(&o_full[i], 1);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const PromptTile f = prompt_find_tile(a, blockIdx.x / a.Hkv, blockIdx.x == 0);
+    if (lane == 0) *s_tile = f;
+  }
+  __syncthreads();
+  const PromptTile t = *s_tile;
+  if (!t.ok) return;
+  if (smem_u32(smem) & 1023u) {              // the swizzle counts on it
+    if (tid == 0) record_error(BITNET_ERR_UNSUPPORTED);
+    return;
+  }
+  if (warp == 17) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (tid == 0) pdl_launch_dependents();
+
+  // the two halves: tokens and key tiles
+  const int half_tokens = a.half_tokens;
+  const int end = min(t.t0 + a.tile_tokens, t.ql);         // the tile may be one half long
+  const int shift = t.kl - t.ql;             // row r sees keys 0 .. r + shift
+  int n_tiles[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int first = t.t0 + i * half_tokens;
+    const int last = min(first + half_tokens, end) - 1;
+    const int keys = last < first ? 0 : max(0, min(t.kl, last + shift + 1));
+    n_tiles[i] = (keys + kPtKeys - 1) / kPtKeys;
+  }
+  const int n_all = max(n_tiles[0], n_tiles[1]);
+
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsIssue));
+    if (warp == 16 && elect_one() && n_all > 0) {
+      // ------------------------------------------------------ TMA producer
+      mbar_arrive_expect_tx(q_full, (uint32_t)(2 * C::kHalves * half_tokens * a.group * 128));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(smem_u32(smem) + (uint32_t)(i * C::kTile + h * C::kBlock), &tq, q_full,
+                      h * 64, kvh * a.group, t.q0 + t.t0 + i * half_tokens);
+      bool ok = true;
+      int u = 0;                             // tiles K_0 V_0 K_1 V_1 ...
+      for (; u < 2 * n_all; ++u) {
+        const int s = u % S;
+        if (u >= S && !mbar_wait(&kv_empty[s], ((u / S) - 1) & 1)) { ok = false; break; }
+        mbar_arrive_expect_tx(&kv_full[s], (uint32_t)C::kTile);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(smem_u32(ring) + (uint32_t)(s * C::kTile + h * C::kBlock),
+                      (u & 1) ? &tv : &tk, &kv_full[s], h * 64, kvh, t.k0 + (u >> 1) * kPtKeys);
+      }
+      // a wait that gave up: the copies in flight still land before the exit
+      if (!ok)
+        for (int w = u > S ? u - S : 0; w < u; ++w) mbar_wait(&kv_full[w % S], (w / S) & 1);
+    } else if (warp == 17 && elect_one() && n_all > 0) {
+      // -------------------------------------------------------- MMA issuer
+      const uint64_t q_desc = sw128_desc(smem_u32(smem)), k_desc = sw128_desc(smem_u32(ring));
+      const uint64_t v_desc = sw128_mn_desc(smem_u32(ring), C::kBlock);
+      auto scores = [&](int i, int s) {      // S_i = Q_i K^T, K in stage s
+        const uint64_t qd = q_desc + (uint64_t)(i * (C::kTile >> 4));
+        const uint64_t kd = k_desc + (uint64_t)(s * (C::kTile >> 4));
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint64_t o = (uint64_t)((x >> 2) * (C::kBlock >> 4) + 2 * (x & 3));
+          tc_mma_bf16(tmem + (uint32_t)(i * kPtKeys), qd + o, kd + o, C::kIdescS, x > 0);
+        }
+        tc_commit(&s_full[i]);
+      };
+      auto outputs = [&](int i, int s, bool add) {   // O_i (+)= P_i V, V in stage s
+        const uint64_t vd = v_desc + (uint64_t)(s * (C::kTile >> 4));
+        const uint32_t ot = tmem + (uint32_t)(2 * kPtKeys + i * D), pt = tmem + (uint32_t)(i * kPtKeys);
+        tc_mma_bf16_ts(ot, pt, vd, C::kIdescO, add);
+#pragma unroll
+        for (int x = 1; x < kPtKeys / 16; ++x)
+          tc_mma_bf16_ts(ot, pt + 8 * x, vd + x * (2048 >> 4), C::kIdescO, 1);
+      };
+      int s = 1;                             // stage and phase of V_j
+      uint32_t ph = 0;
+      bool ok = mbar_wait(q_full, 0) && mbar_wait(&kv_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (n_tiles[i] > 0) scores(i, 0);
+        tc_commit(&kv_empty[0]);
+      }
+      for (int j = 0; j < n_all && ok; ++j) {
+        const int sk = s + 1 == S ? 0 : s + 1;               // K_{j+1}
+        const uint32_t phk = s + 1 == S ? ph ^ 1 : ph;
+        const bool more = j + 1 < n_all;
+        ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // one half's two products, then the other's: the halves fall into
+          // step with one in the softmax while the other is here
+          if (!ok || j >= n_tiles[i]) continue;
+          ok = mbar_wait(&p_full[i], (uint32_t)(j & 1));
+          if (!ok) continue;
+          tc_fence_after();
+          outputs(i, s, j > 0);
+          if (j + 1 < n_tiles[i])
+            scores(i, sk);
+          else
+            tc_commit(&o_full[i]);
+        }
+        if (ok) {
+          tc_commit(&kv_empty[s]);
+          if (more) tc_commit(&kv_empty[sk]);
+        }
+        s = sk + 1 == S ? 0 : sk + 1;
+        ph = sk + 1 == S ? phk ^ 1 : phk;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoftmax));
+    const int i = warp >> 3, cg = (warp >> 2) & 1;       // row half, column half
+    const int r = 32 * (warp & 3) + lane;    // this thread's row
+    const int pair = 1 + 4 * i + (warp & 3);
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t st = tmem + lanes + (uint32_t)(i * kPtKeys + cg * 64);
+    const uint32_t pt = tmem + lanes + (uint32_t)(i * kPtKeys + cg * 32);
+    const uint32_t ot = tmem + lanes + (uint32_t)(2 * kPtKeys + i * D + cg * (D / 2));
+    float* mine = exch + (2 * i + cg) * 128 + r;
+    const float* other = exch + (2 * i + (cg ^ 1)) * 128 + r;
+    const int n = i ? n_tiles[1] : n_tiles[0];
+    const int first = t.t0 + i * half_tokens;
+    const int token = first + r / a.group;
+    const int lim = token + shift - cg * 64; // last key the row sees, from this column half
+    const float c = a.scale_log2;
+    const uint64_t c2 = f2_pack(c, c);
+    const float slack = 8.0f / c;
+    float m = -INFINITY;
+    uint64_t l2[2] = {0, 0};                 // partial sums, two lanes each
+    // a wait that gave up does not end the loop: both warps of a pair go on to
+    // the same barriers (without further waits) and nothing is written
+    bool ok = true, poison = false;
+    for (int j = 0; j < n; ++j) {
+      if (ok) ok = mbar_wait(&s_full[i], (uint32_t)(j & 1));
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const bool border = j * kPtKeys + kPtKeys - 1 > first + shift;   // some row ends inside
+      const int e = lim - j * kPtKeys;
+      while (true) {
+        const float neg = m == -INFINITY ? 0.0f : -m * c;
+        const uint64_t neg2 = f2_pack(neg, neg);
+        uint32_t s[64], p[32];
+        float mx[2] = {-INFINITY, -INFINITY};
+        uint64_t t2[2] = {0, 0};
+        tmem_ld32_async(st, s);
+        tmem_ld32_async(st + 32, s + 32);
+        tmem_wait_ld(s);
+        tmem_wait_ld(s + 32);
+        if (border) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (x > e) s[x] = 0xff800000u;
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
+          mx[x & 1] = max3_nan(mx[x & 1], s0, s1);
+          const uint64_t y = f2_fma(f2_pack(s0, s1), c2, neg2);
+          float e0, e1;
+          if ((x * kPtEmulated) % 8 < kPtEmulated) {
+            f2_unpack(ex2_pair(y), e0, e1);
+          } else {
+            f2_unpack(y, e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+          }
+          p[x] = pack_bf16(e0, e1);
+          t2[x & 1] = f2_add(t2[x & 1], f2_pack(e0, e1));
+        }
+        const float top = max3_nan(mx[0], mx[1], mx[1]);
+        // the vote also says that both warps have read their scores, which P
+        // is about to overwrite
+        if (pair_any(pair, top > m + slack)) {
+          // a row has outgrown its reference (or had none): once more with it
+          *mine = top;
+          pair_sync(pair);
+          const float both = fmaxf(top, *other);
+          const float to = both > m + slack ? both : m;
+          const float f = to == m ? 1.0f : ex2((m - to) * c);
+          m = to;
+          if (j > 0) {
+            const uint64_t f2 = f2_pack(f, f);
+            l2[0] = f2_fma(l2[0], f2, 0);
+            l2[1] = f2_fma(l2[1], f2, 0);
+#pragma unroll
+            for (int x = 0; x < D / 2; x += 32) {
+              uint32_t o[32];
+              tmem_ld32_async(ot + x, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32_async(ot + x, o);
+            }
+          }
+          continue;
+        }
+        poison |= !(top < INFINITY);
+        tmem_st32_async(pt, p);
+        l2[0] = f2_add(l2[0], t2[0]);
+        l2[1] = f2_add(l2[1], t2[1]);
+        break;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i]);
+    }
+    // ------------------------------------------------------------ epilogue
+    float l, l1;
+    f2_unpack(f2_add(l2[0], l2[1]), l, l1);
+    l += l1;
+    *mine = l;
+    pair_sync(pair);
+    l += *other;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (n > 0)
+      ok = ok && mbar_wait(&o_full[i], 0);
+    else if (n_all > 0)
+      ok = mbar_wait(q_full, 0);             // the copy into what becomes the staging area
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    // through shared memory (the half's Q tile, which every MMA has read) so
+    // that whole segments of D / 2 values are written at a time; 16-byte chunks
+    // are xored with the row
+    constexpr int CH = D / 16;               // chunks per segment
+    const int rows = (min(first + half_tokens, end) - first) * a.group;   // may be <= 0
+    const uint32_t stage = smem_u32(smem) + (uint32_t)(i * C::kTile + (warp & 7) * 32 * D);
+    auto at = [&](int row, int ch) {
+      return stage + (uint32_t)(row * D + ((ch ^ ((row * CH / 8) & (CH - 1))) << 4));
+    };
+    float odd = 0.0f;
+#pragma unroll
+    for (int x = 0; x < D / 2; x += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32_async(ot + x, o);
+        tmem_wait_ld(o);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = 0;
+      }
+#pragma unroll
+      for (int y = 0; y < 32; y += 8) {
+        float f[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          f[z] = __uint_as_float(o[y + z]) * inv;
+          odd = fmaf(f[z], 0.0f, odd);
+        }
+        sts_v4(at(lane, (x + y) / 8), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                 pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+      }
+    }
+    __syncwarp();
+    const int r0 = 32 * (warp & 3);
+    if (ok) {
+#pragma unroll 4
+      for (int x = lane; x < 32 * CH; x += 32) {
+        const int rr = x / CH, ch = x % CH, row = r0 + rr;
+        if (row < rows) {
+          const int tok = row / a.group, head = kvh * a.group + row % a.group;
+          *reinterpret_cast<uint4*>(a.y + (int64_t)(t.q0 + first + tok) * a.y_stride +
+                                    (int64_t)head * D + cg * (D / 2) + ch * 8) = lds_v4(at(rr, ch));
+        }
+      }
+      if (a.lse && cg == 0 && r < rows)
+        a.lse[(int64_t)(t.q0 + token) * a.Hq + kvh * a.group + r % a.group] =
+            l == 0.0f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+    }
+    // rows with a result that is not finite are done again, the pair's warps
+    // taking turns; both warps' stores come first
+    const bool again = pair_any(pair, ok && r < rows && (poison || odd != odd));
+    if (again) {
+      *mine = ok && r < rows && (poison || odd != odd) ? 1.0f : 0.0f;
+      pair_sync(pair);
+      unsigned redo = __ballot_sync(0xffffffffu, *mine + *other > 0.0f);
+      for (int k = 0; redo; ++k) {
+        const int row = r0 + __ffs(redo) - 1;
+        redo &= redo - 1;
+        if ((k & 1) == cg)
+          prompt_row_by_warp<D>(a, t, first + row / a.group, kvh * a.group + row % a.group);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
   }
 }
 
