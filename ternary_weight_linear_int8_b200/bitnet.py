@@ -11,7 +11,6 @@ tensors holding the bit patterns.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -580,55 +579,71 @@ def bitnet_ffn_tp_finish(acc, I, gamma_down, amax2, sumsq_x, sumsq_h, eps=1e-5, 
 
 
 # ------------------------------------------------- attention and its cache
-def _on(t):
-    """(context of) the device of t, for tensors that are not on the current one."""
-    d = t.device.index
-    return _HERE_CTX if d == torch.cuda.current_device() else torch.cuda.device(d)
+# These calls take a few microseconds on the device, so their marshalling is
+# kept short: device ordinals instead of device objects, the raw stream handle
+# instead of a stream object.
+_BITS16 = (torch.bfloat16, torch.int16, torch.float16, torch.uint16)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-_HERE_CTX = contextlib.nullcontext()
+def _run(name, dev, *args):
+    """Call the entry point `name` on device ordinal `dev` and its current stream."""
+    fn = getattr(_lib or lib(), name)
+    if _current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    if st != 0:
+        raise BitnetError(name, st)
 
 
-def _heads(t, name, device):
-    """A [tokens, heads, D] bf16 tensor on `device`, heads contiguous, any token stride."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dim() != 3 or t.element_size() != 2:
+def _heads(t, name, dev):
+    """A [tokens, heads, D] bf16 tensor on device ordinal `dev`, heads contiguous, any token
+    stride.  Returns that stride."""
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
+    if t.dim() != 3 or t.dtype not in _BITS16:
         raise ValueError(f"{name} must be [tokens, heads, D] with 16-bit (bf16) elements")
     n, h, d = t.shape
-    st = t.stride()
-    if n < 1 or (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
+    s0, s1, s2 = t.stride()
+    if n < 1 or (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name} must have contiguous heads and at least one token")
-    return st[0] if n > 1 else max(st[0], h * d)
+    return s0 if n > 1 else h * d
 
 
-def _pages(t, name, pool, device):
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    if t.element_size() != 2 or t.dim() != 4 or t.shape[0] != pool.n_pages or \
-            t.shape[2] != pool.page_size:
+def _pages(t, name, pool, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the pool's device")
+    s = t.shape
+    if len(s) != 4 or t.dtype not in _BITS16 or s[0] != pool.n_pages or s[2] != pool.page_size:
         raise ValueError(f"{name} must be [n_pages, heads, page_size, D] with 16-bit elements")
-    return t
+    return s
 
 
-def _index(t, name, device, n=None):
-    """An int32 vector on `device` (None passes)."""
+def _index(t, name, dev, n=None):
+    """The address of an int32 vector on device ordinal `dev` (None: a null pointer)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.dim() != 1:
-        raise ValueError(f"{name} must be a contiguous int32 vector on {device}")
+    if t.dtype != torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector on the same device")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements")
+    return t.data_ptr()
+
+
+def _like(t, name, shape, dtypes, dev):
+    """Checks an output given by the caller (contiguous unless checked further)."""
+    if t.get_device() != dev or tuple(t.shape) != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name} must have shape {list(shape)} and the right type, on the same device")
     return t
 
 
-def _out(t, name, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.device != device or tuple(t.shape) != tuple(shape) or \
-            t.element_size() != torch.empty((), dtype=dtype).element_size():
-        raise ValueError(f"{name} must have shape {list(shape)} on {device}")
-    return t
+def _lse_out(lse, want, shape, dev, device):
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=device) if want else None
+    return _dev(_like(lse, "lse", shape, (torch.float32,), dev), "lse")
 
 
 def bitnet_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -636,24 +651,23 @@ def bitnet_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
     """Causal attention over packed prompts: q [Tq,Hq,D], k and v [Tk,Hkv,D] bf16, sequence i in
     rows cu_q[i] .. cu_q[i+1] and keys cu_k[i] .. (None: cu_q).  scale defaults to D ** -0.5.
     Rows outside all sequences are left as they are.  Returns (y [Tq,Hq,D], lse [Tq,Hq] or None)."""
-    dev = q.device
+    dev = q.get_device()
     qs, ks, vs = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
     Tq, Hq, D = q.shape
     Tk, Hkv, Dk = k.shape
     if Dk != D or v.shape != k.shape:
         raise ValueError("k and v must be [Tk, Hkv, D] with q's D")
-    _index(cu_q, "cu_q", dev)
-    cu_k = cu_q if cu_k is None else _index(cu_k, "cu_k", dev, cu_q.numel())
-    y = _out(y, "y", (Tq, Hq, D), torch.bfloat16, dev)
-    ys = _heads(y, "y", dev)
+    cq = _index(cu_q, "cu_q", dev)
+    n = cu_q.numel()
+    ck = cq if cu_k is None else _index(cu_k, "cu_k", dev, n)
+    if y is None:
+        y = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+    ys = _heads(_like(y, "y", (Tq, Hq, D), _BITS16, dev), "y", dev)
     if want_lse or lse is not None:
-        lse = _dev(_out(lse, "lse", (Tq, Hq), torch.float32, dev), "lse")
-    with _on(q):
-        st = lib().bitnet_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                      cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1, Tq, Tk,
-                                      Hq, Hkv, D, D ** -0.5 if scale is None else scale,
-                                      y.data_ptr(), ys, _ptr(lse), _stream())
-    _check("bitnet_attn_prompt", st)
+        lse = _lse_out(lse, want_lse, (Tq, Hq), dev, q.device)
+    _run("bitnet_attn_prompt", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck,
+         n - 1, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else scale, y.data_ptr(), ys,
+         None if lse is None else lse.data_ptr())
     return y, lse
 
 
@@ -665,11 +679,22 @@ class KvPool:
     def __init__(self, buf, n_slots, max_pages, n_pages, page_size, ws=None):
         self.buf, self.page_size, self.ws = buf, page_size, ws
         self.n_slots, self.max_pages, self.n_pages = n_slots, max_pages, n_pages
-        a, b = n_slots * max_pages, n_slots * max_pages + n_slots
-        self.table, self.lens, self.refs = buf[:a].view(n_slots, max_pages), buf[a:b], buf[b:]
-        p = buf.data_ptr()
-        self.c = KvTables(p, p + 4 * a, p + 4 * b, n_slots, max_pages, n_pages, page_size)
-        self.ref = ctypes.byref(self.c)
+        self.dev = buf.get_device()
+        a, p = n_slots * max_pages, buf.data_ptr()
+        self.c = KvTables(p, p + 4 * a, p + 4 * (a + n_slots), n_slots, max_pages, n_pages, page_size)
+        self.ref = ctypes.addressof(self.c)
+
+    @property
+    def table(self):
+        return self.buf.as_strided((self.n_slots, self.max_pages), (self.max_pages, 1), 0)
+
+    @property
+    def lens(self):
+        return self.buf.as_strided((self.n_slots,), (1,), self.n_slots * self.max_pages)
+
+    @property
+    def refs(self):
+        return self.buf.as_strided((self.n_pages,), (1,), self.n_slots * (self.max_pages + 1))
 
     def clone(self):
         """A copy of the tables (the pages are not part of a pool).  The copy shares the
@@ -689,49 +714,41 @@ def bitnet_kv_pool(n_slots: int, max_pages: int, n_pages: int, page_size: int,
     nb = lib().bitnet_kv_workspace_size(n_slots, n_pages)
     if nb == 0 or max_pages < 1:
         raise ValueError("n_slots, max_pages or n_pages out of range")
-    buf = torch.empty(n_slots * max_pages + n_slots + n_pages, dtype=torch.int32, device=device)
-    if not buf.is_cuda:
+    if torch.device(device).type != "cuda":
         raise ValueError("device must be a CUDA device")
+    buf = torch.zeros(n_slots * max_pages + n_slots + n_pages, dtype=torch.int32, device=device)
     pool = KvPool(buf, n_slots, max_pages, n_pages, page_size,
                   torch.empty(nb, dtype=torch.uint8, device=device))
     pool.table.fill_(-1)
-    pool.lens.zero_()
-    pool.refs.zero_()
     return pool
 
 
 def bitnet_kv_extend(pool: KvPool, add: torch.Tensor, slots=None, short_pages=None):
     """Sequences (slots, or 0, 1, ...) grow by add[i] tokens.  short_pages (optional int32 [1])
     receives 0, the lacking pages or -1."""
-    dev = pool.buf.device
-    _index(add, "add", dev)
-    _index(slots, "slots", dev, add.numel())
-    _index(short_pages, "short_pages", dev, 1)
-    with _on(pool.buf):
-        st = lib().bitnet_kv_extend(pool.ref, _ptr(slots), add.data_ptr(), add.numel(),
-                                    _ptr(short_pages), pool.ws.data_ptr(), pool.ws.numel(),
-                                    _stream())
-    _check("bitnet_kv_extend", st)
+    dev, ws = pool.dev, pool.ws
+    n = add.numel()
+    ap = _index(add, "add", dev)
+    _run("bitnet_kv_extend", dev, pool.ref, _index(slots, "slots", dev, n), ap, n,
+         _index(short_pages, "short_pages", dev, 1), ws.data_ptr(), ws.numel())
 
 
 def bitnet_kv_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, pool: KvPool,
                      k_pages: torch.Tensor, v_pages: torch.Tensor, slots=None):
     """Rows cu[b] .. cu[b+1] of k and v [T,Hkv,D] become the last tokens of slot b (slots[b])."""
-    dev = pool.buf.device
+    dev = pool.dev
     ks, vs = _heads(k, "k", dev), _heads(v, "v", dev)
-    T, Hkv, D = k.shape
-    if v.shape != k.shape:
+    shape = k.shape
+    T, Hkv, D = shape
+    if v.shape != shape:
         raise ValueError("k and v must have one shape")
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if _pages(t, name, pool, dev).shape[1] != Hkv or t.shape[3] != D:
-            raise ValueError(f"{name} must have k's heads and D")
-    _index(cu, "cu", dev)
-    _index(slots, "slots", dev, cu.numel() - 1)
-    with _on(pool.buf):
-        st = lib().bitnet_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, cu.data_ptr(), _ptr(slots),
-                                    cu.numel() - 1, T, Hkv, D, pool.ref, k_pages.data_ptr(),
-                                    v_pages.data_ptr(), _stream())
-    _check("bitnet_kv_append", st)
+    s = _pages(k_pages, "k_pages", pool, dev)
+    if _pages(v_pages, "v_pages", pool, dev) != s or s[1] != Hkv or s[3] != D:
+        raise ValueError("k_pages and v_pages must have k's heads and D")
+    n = cu.numel() - 1
+    _run("bitnet_kv_append", dev, k.data_ptr(), ks, v.data_ptr(), vs, _index(cu, "cu", dev),
+         _index(slots, "slots", dev, n), n, T, Hkv, D, pool.ref, k_pages.data_ptr(),
+         v_pages.data_ptr())
 
 
 def bitnet_attn_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -743,95 +760,97 @@ def bitnet_attn_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
                        workspace=None):
     """One new token per sequence over the paged cache: q [B,Hq,D], row b reads slot b (slots[b]).
     Returns (y [B,Hq,D], lse [B,Hq] or None)."""
-    dev = pool.buf.device
+    dev = pool.dev
     qs = _heads(q, "q", dev)
-    B, Hq, D = q.shape
-    if _pages(k_pages, "k_pages", pool, dev).shape != _pages(v_pages, "v_pages", pool, dev).shape \
-            or k_pages.shape[3] != D:
+    shape = q.shape
+    B, Hq, D = shape
+    s = _pages(k_pages, "k_pages", pool, dev)
+    if _pages(v_pages, "v_pages", pool, dev) != s or s[3] != D:
         raise ValueError("k_pages and v_pages must have one shape with q's D")
-    Hkv = k_pages.shape[1]
-    _index(slots, "slots", dev, B)
-    y = _out(y, "y", (B, Hq, D), torch.bfloat16, dev)
-    ys = _heads(y, "y", dev)
+    Hkv = s[1]
+    sp = _index(slots, "slots", dev, B)
+    if y is None:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    ys = _heads(_like(y, "y", (B, Hq, D), _BITS16, dev), "y", dev)
     if want_lse or lse is not None:
-        lse = _dev(_out(lse, "lse", (B, Hq), torch.float32, dev), "lse")
-    nb = lib().bitnet_attn_decode_workspace_size(B, Hq, Hkv, D)
-    ws = _workspace(nb, dev, workspace)
-    with _on(q):
-        st = lib().bitnet_attn_decode(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
-                                      pool.ref, _ptr(slots), B, Hq, Hkv, D,
-                                      D ** -0.5 if scale is None else scale, y.data_ptr(), ys,
-                                      _ptr(lse), _ptr(ws), nb, _stream())
-    _check("bitnet_attn_decode", st)
+        lse = _lse_out(lse, want_lse, (B, Hq), dev, q.device)
+    if workspace is None:
+        nb = lib().bitnet_attn_decode_workspace_size(B, Hq, Hkv, D)
+        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    _run("bitnet_attn_decode", dev, q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
+         pool.ref, sp, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, y.data_ptr(), ys,
+         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return y, lse
+
+
+def _pair_list(pairs, n_pairs, n, dev, device):
+    if pairs is None:
+        pairs = torch.empty((n, 2), dtype=torch.int32, device=device)
+    else:
+        _dev(_like(pairs, "pairs", (n, 2), (torch.int32,), dev), "pairs")
+    if n_pairs is None:
+        n_pairs = torch.empty(1, dtype=torch.int32, device=device)
+    else:
+        _like(n_pairs, "n_pairs", (1,), (torch.int32,), dev)
+    return pairs, n_pairs
 
 
 def bitnet_kv_fork(pool: KvPool, parents: torch.Tensor, children: torch.Tensor, short_pages=None,
                    pairs=None, n_pairs=None):
     """Slots children[i] become copies of parents[i].  Returns (pairs [n,2], n_pairs [1]): the page
     copies that bitnet_kv_copy_pages has to make in every layer."""
-    dev = pool.buf.device
-    _index(parents, "parents", dev)
+    dev, ws = pool.dev, pool.ws
     n = parents.numel()
-    _index(children, "children", dev, n)
-    _index(short_pages, "short_pages", dev, 1)
-    pairs = _dev(_out(pairs, "pairs", (n, 2), torch.int32, dev), "pairs")
-    n_pairs = _out(n_pairs, "n_pairs", (1,), torch.int32, dev)
-    with _on(pool.buf):
-        st = lib().bitnet_kv_fork(pool.ref, parents.data_ptr(), children.data_ptr(), n,
-                                  pairs.data_ptr(), n_pairs.data_ptr(), _ptr(short_pages),
-                                  pool.ws.data_ptr(), pool.ws.numel(), _stream())
-    _check("bitnet_kv_fork", st)
+    pp, cp = _index(parents, "parents", dev), _index(children, "children", dev, n)
+    pairs, n_pairs = _pair_list(pairs, n_pairs, n, dev, pool.buf.device)
+    _run("bitnet_kv_fork", dev, pool.ref, pp, cp, n, pairs.data_ptr(), n_pairs.data_ptr(),
+         _index(short_pages, "short_pages", dev, 1), ws.data_ptr(), ws.numel())
     return pairs, n_pairs
 
 
 def bitnet_kv_free(pool: KvPool, slots: torch.Tensor):
     """Free slots: their pages' counts drop, their rows become empty."""
-    _index(slots, "slots", pool.buf.device)
-    with _on(pool.buf):
-        st = lib().bitnet_kv_free(pool.ref, slots.data_ptr(), slots.numel(), _stream())
-    _check("bitnet_kv_free", st)
+    sp = _index(slots, "slots", pool.dev)
+    _run("bitnet_kv_free", pool.dev, pool.ref, sp, slots.numel())
 
 
 def bitnet_kv_compact(pool: KvPool, live=None, pairs=None, n_pairs=None):
     """Move the pages in use to the front of the pool.  Returns (pairs, n_pairs) for
     bitnet_kv_copy_pages; live (optional int32 [1]) receives the number of pages in use."""
-    dev = pool.buf.device
-    _index(live, "live", dev, 1)
-    shape = (max(1, pool.n_pages // 2), 2)
-    pairs = _dev(_out(pairs, "pairs", shape, torch.int32, dev), "pairs")
-    n_pairs = _out(n_pairs, "n_pairs", (1,), torch.int32, dev)
-    with _on(pool.buf):
-        st = lib().bitnet_kv_compact(pool.ref, pairs.data_ptr(), n_pairs.data_ptr(), _ptr(live),
-                                     pool.ws.data_ptr(), pool.ws.numel(), _stream())
-    _check("bitnet_kv_compact", st)
+    dev, ws = pool.dev, pool.ws
+    pairs, n_pairs = _pair_list(pairs, n_pairs, max(1, pool.n_pages // 2), dev, pool.buf.device)
+    _run("bitnet_kv_compact", dev, pool.ref, pairs.data_ptr(), n_pairs.data_ptr(),
+         _index(live, "live", dev, 1), ws.data_ptr(), ws.numel())
     return pairs, n_pairs
 
 
 def bitnet_kv_copy_pages(k_pages, v_pages, pairs: torch.Tensor, n_pairs: torch.Tensor):
     """Make the listed page copies in every layer: k_pages, v_pages are lists of the layers'
     [n_pages, Hkv, page_size, D] tensors, all of one shape."""
-    if len(k_pages) != len(v_pages) or not k_pages:
-        raise ValueError("k_pages and v_pages must be non-empty lists of equal length")
-    first = k_pages[0]
-    dev, shape = first.device, first.shape
     L = len(k_pages)
-    for t in (*k_pages, *v_pages):
-        if t.shape != shape or t.device != dev or t.element_size() != 2 or not t.is_cuda or \
-                not t.is_contiguous():
-            raise ValueError("all pages must be contiguous 16-bit CUDA tensors of one shape")
-    _index(n_pairs, "n_pairs", dev, 1)
+    if len(v_pages) != L or not L:
+        raise ValueError("k_pages and v_pages must be non-empty lists of equal length")
+    shape, dev = k_pages[0].shape, n_pairs.get_device()
+    if len(shape) != 4:
+        raise ValueError("pages must be [n_pages, heads, page_size, D]")
+    ptrs = []
+    for ts in (k_pages, v_pages):
+        for t in ts:
+            if t.shape != shape or t.get_device() != dev or t.dtype not in _BITS16 or \
+                    not t.is_contiguous():
+                raise ValueError("all pages must be contiguous 16-bit CUDA tensors of one shape")
+            ptrs.append(t.data_ptr())
+    np_ = _index(n_pairs, "n_pairs", dev, 1)
     if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or \
-            pairs.device != dev or not pairs.is_contiguous():
+            pairs.get_device() != dev or not pairs.is_contiguous():
         raise ValueError("pairs must be a contiguous [n, 2] int32 tensor")
-    K = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_pages])
-    V = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_pages])
-    page_bytes = first[0].numel() * 2
-    with _on(first):
-        st = lib().bitnet_kv_copy_pages(L, K, V, shape[0], page_bytes, pairs.data_ptr(),
-                                        n_pairs.data_ptr(), min(pairs.shape[0], shape[0]),
-                                        _stream())
-    _check("bitnet_kv_copy_pages", st)
+    both = (ctypes.c_void_p * (2 * L))(*ptrs)
+    at = ctypes.addressof(both)
+    n, h, s, d = shape
+    _run("bitnet_kv_copy_pages", dev, L, at, at + 8 * L, n, h * s * d * 2, pairs.data_ptr(), np_,
+         min(pairs.shape[0], n))
 
 
 def bitnet_last_device_status() -> int:
