@@ -95,9 +95,12 @@ bitnet_status decode_launch(const AttnDecodeArgs& a, int ctas, cudaStream_t s) {
   if (launch_pdl(attn_decode_kernel<D, NT>, (unsigned)ctas, kDecWarps * 32, smem, s, a) !=
       cudaSuccess)
     return BITNET_ERR_CUDA;
-  const int64_t blocks = ((int64_t)a.B * a.Hq + 3) / 4;
-  if (launch_pdl(attn_join_kernel<D>, (unsigned)blocks, 128, 0, s, a, ctas) != cudaSuccess)
-    return BITNET_ERR_CUDA;
+  const int64_t heads = (int64_t)a.B * a.Hq;
+  const cudaError_t e =
+      heads <= 4 * ctas
+          ? launch_pdl(attn_join_kernel<D, 4>, (unsigned)heads, 128, 0, s, a, ctas)
+          : launch_pdl(attn_join_kernel<D, 1>, (unsigned)((heads + 3) / 4), 128, 0, s, a, ctas);
+  if (e != cudaSuccess) return BITNET_ERR_CUDA;
   return BITNET_OK;
 }
 

@@ -169,26 +169,33 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const At
   const uint32_t ring = smem_u32(dsm) + (uint32_t)(warp * kDecStages * kStage);
   int loaded = 0;
   uint32_t bad = 0;                          // bit s: stage s holds no page's tokens
+  // The page of this warp's tokens in the load cursor's unit is looked up one
+  // unit ahead, so that no copy waits for the table.
+  int ld_page = -1, ld_row = 0;
+  auto look_up = [&]() {
+    const int pos = ld.chunk * kDecUnit + warp * 16;
+    ld_page = -1;
+    if (loaded < units && pos < ld.len) {
+      const int e = pos / a.kv.page_size;
+      ld_row = pos - e * a.kv.page_size;
+      ld_page = a.kv.table[(int64_t)ld.slot * a.kv.max_pages + e];
+    }
+  };
+  look_up();
   // Request this warp's 16 tokens of the load cursor's unit.  Rows behind the
   // sequence's end and pages outside the pool are zero in shared memory (and
   // masked below), so nothing the cache holds there can reach a sum.
   auto load = [&]() {
     if (loaded < units) {
       const int pos = ld.chunk * kDecUnit + warp * 16;
-      const int kvh = ld.vh / a.hb;
-      int page = -1, row = 0;
-      if (pos < ld.len) {
-        const int e = pos / a.kv.page_size;
-        row = pos - e * a.kv.page_size;
-        page = a.kv.table[(int64_t)ld.slot * a.kv.max_pages + e];
-        if (page >= a.kv.n_pages) page = -1;
-        if (page < 0 && lane == 0) record_error(BITNET_ERR_PAGES);
-      }
-      const int left = page < 0 ? 0 : ld.len - pos;
+      const int kvh = a.hb == 1 ? ld.vh : ld.vh / a.hb;
+      const bool no_page = ld_page < 0 || ld_page >= a.kv.n_pages;
+      if (no_page && pos < ld.len && lane == 0) record_error(BITNET_ERR_PAGES);
+      const int left = no_page ? 0 : ld.len - pos;
       const uint32_t bit = 1u << (loaded % kDecStages);
-      bad = page < 0 ? bad | bit : bad & ~bit;
-      const int64_t off =
-          (((int64_t)(page < 0 ? 0 : page) * a.Hkv + kvh) * a.kv.page_size + row) * D;
+      bad = no_page ? bad | bit : bad & ~bit;
+      const int64_t off = no_page ? 0
+                                  : (((int64_t)ld_page * a.Hkv + kvh) * a.kv.page_size + ld_row) * D;
       const uint32_t dst = ring + (uint32_t)((loaded % kDecStages) * kStage);
       const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.k_pages + off);
       const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.v_pages + off);
@@ -203,6 +210,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const At
       ld.next(a);
     }
     ++loaded;
+    look_up();
     cp_async_commit();
   };
 #pragma unroll
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const At
   bool first_piece = true;
   bool fresh = true;                         // at the start of a piece
   for (int u = 0; u < units; ++u) {
-    const int kvh = cur.vh / a.hb, hblk = cur.vh % a.hb;
+    const int kvh = a.hb == 1 ? cur.vh : cur.vh / a.hb, hblk = cur.vh - kvh * a.hb;
     const int heads = min(a.rows, a.group - hblk * a.rows);
     const int head0 = kvh * a.group + hblk * a.rows;
     if (fresh) {
@@ -398,55 +406,101 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const At
 
 // Joins the pieces of (sequence, head) pairs that several CTAs shared, in the
 // order of their units, and writes the rows of empty sequences (0, and -inf
-// for the log-sum).  One warp per query head.
-template <int D>
+// for the log-sum).  SPLIT warps per query head: the pieces are dealt to them
+// in turn, each takes up to 32 at a time (a lane has one piece's maximum and
+// sum, a column set per lane for the outputs), and with four warps the last
+// step is over shared memory.  Four warps where there are few heads, which
+// then have many pieces: 64 heads of 37 pieces took 28 us with one warp each
+// and a division per piece.
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnDecodeArgs a, int ctas) {
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  constexpr int V = D / 32;                  // outputs per lane
+  __shared__ float s_acc[SPLIT][D], s_ml[SPLIT][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = SPLIT == 1 ? 0 : warp;
+  const int64_t id = SPLIT == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
   pdl_wait();
   if (id >= (int64_t)a.B * a.Hq) return;
   const int b = (int)(id / a.Hq), head = (int)(id % a.Hq);
-  uint16_t* yr = a.y + (int64_t)b * a.y_stride + (int64_t)head * D;
-  const long long W = a.first_unit[a.B], G = min((long long)ctas, W), at = a.first_unit[b], VH = (long long)a.Hkv * a.hb;
-  const long long chunks = (a.first_unit[b + 1] - at) / VH;
-  constexpr int V = D / 32;                  // outputs per lane
+  uint16_t* yr = a.y + (int64_t)b * a.y_stride + (int64_t)head * D + lane * V;
+  const long long W = a.first_unit[a.B], at = a.first_unit[b], to = a.first_unit[b + 1];
+  const int chunks = (int)(to - at) / (a.Hkv * a.hb);
   if (chunks == 0) {
+    if (part == 0) {
 #pragma unroll
-    for (int i = 0; i < V; i += 2) *reinterpret_cast<uint32_t*>(yr + lane * V + i) = 0u;
-    if (a.lse && lane == 0) a.lse[id] = -INFINITY;
+      for (int i = 0; i < V; i += 2) *reinterpret_cast<uint32_t*>(yr + i) = 0u;
+      if (a.lse && lane == 0) a.lse[id] = -INFINITY;
+    }
     return;
   }
+  const long long G = min((long long)ctas, W);
   const int kvh = head / a.group, in_group = head % a.group;
   const int vh = kvh * a.hb + in_group / a.rows, row = in_group % a.rows;
-  const long long ua = at + (long long)vh * chunks, ub = ua + chunks;
-  const long long c0 = ((ua + 1) * G - 1) / W, c1 = (ub * G - 1) / W;
+  const long long ua = at + (long long)vh * chunks;
+  const int c0 = (int)(((ua + 1) * G - 1) / W), c1 = (int)(((ua + chunks) * G - 1) / W);
   if (c0 == c1) return;                      // finished by its CTA
-  float top = -INFINITY;
-  for (long long c = c0 + lane; c <= c1; c += 32) {
-    const long long ps = 2 * c + (W * c / G >= ua ? 0 : 1);
-    top = fmaxf(top, a.part_ml[(ps * a.rows + row) * 2]);
-  }
-  top = warp_max(top);
-  float acc[V], sum = 0.f;
+  // CTA c0 holds its piece as its last one unless it starts with it, the
+  // others as their first one
+  const int first_slot = W * c0 / G == ua ? 2 * c0 : 2 * c0 + 1;
+  float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (long long c = c0; c <= c1; ++c) {
-    const long long ps = 2 * c + (W * c / G >= ua ? 0 : 1);
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (ps * a.rows + row) * 2);
-    const float f = ml.x == top ? 1.f : ex2(ml.x - top);
-    sum += f * ml.y;
-    const float* p = a.part + (ps * a.rows + row) * D + lane * V;
+  for (int p0 = part; p0 <= c1 - c0; p0 += 32 * SPLIT) {
+    const int p = p0 + lane * SPLIT;
+    const int slot = p == 0 ? first_slot : 2 * (c0 + p);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (p <= c1 - c0)
+      ml = *reinterpret_cast<const float2*>(a.part_ml + ((int64_t)slot * a.rows + row) * 2);
+    const float t = fmaxf(top, warp_max(ml.x));
+    const float f0 = top == t ? 1.f : ex2(top - t), f = ml.x == t ? 1.f : ex2(ml.x - t);
+    top = t;
+    sum = sum * f0 + f * ml.y;               // per lane until the end
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 t = *reinterpret_cast<const float2*>(p + i);
-      acc[i] += f * t.x;
-      acc[i + 1] += f * t.y;
+    for (int i = 0; i < V; ++i) acc[i] *= f0;
+    const int n = min(32, (c1 - c0 - p0) / SPLIT + 1);
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+      const float fx = __shfl_sync(0xffffffffu, f, x);
+      const int sx = __shfl_sync(0xffffffffu, slot, x);
+      const float* w = a.part + ((int64_t)sx * a.rows + row) * D + lane * V;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(w + i);
+        acc[i] += fx * v.x;
+        acc[i + 1] += fx * v.y;
+      }
     }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (SPLIT > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_acc[part][lane * V + i] = acc[i];
+    if (lane == 0) {
+      s_ml[part][0] = top;
+      s_ml[part][1] = sum;
+    }
+    __syncthreads();
+    if (part != 0) return;
+    float all = s_ml[0][0];
+#pragma unroll
+    for (int w = 1; w < SPLIT; ++w) all = fmaxf(all, s_ml[w][0]);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) {
+      const float f = s_ml[w][0] == all ? 1.f : ex2(s_ml[w][0] - all);
+      sum += f * s_ml[w][1];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += f * s_acc[w][lane * V + i];
+    }
+    top = all;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(yr + lane * V + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(yr + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
   if (a.lse && lane == 0)
     a.lse[id] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
