@@ -321,8 +321,8 @@ bitnet_status bitnet_kv_append(const uint16_t* k, int64_t k_stride, const uint16
   a.kv = device_tables(kv);
   a.k_pages = k_pages; a.v_pages = v_pages;
   a.k_stride = k_stride; a.v_stride = v_stride;
-  a.B = (int)B; a.T = (int)T; a.Hkv = (int)Hkv; a.head_chunks = (int)(D / 8);
-  return launch_pdl(kv_append_kernel, (unsigned)((T + 7) / 8), 256, 0, as_stream(stream), a) ==
+  a.B = (int)B; a.T = (int)T; a.Hkv = (int)Hkv;
+  return launch_pdl(D == 64 ? kv_append_kernel<64> : kv_append_kernel<128>, (unsigned)((T + 7) / 8), 256, 0, as_stream(stream), a) ==
                  cudaSuccess
              ? BITNET_OK : BITNET_ERR_CUDA;
 }

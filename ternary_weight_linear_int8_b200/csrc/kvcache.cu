@@ -58,14 +58,52 @@ __device__ __forceinline__ bool set_bit(uint32_t* bits, int i) {   // true if it
   return (atomicOr(&bits[i >> 5], 1u << (i & 31)) >> (i & 31)) & 1u;
 }
 
+// The entries of one row's new tokens, [e0, e1) of slot s.
+struct NewEntries {
+  int s, e0, e1;
+};
+// Calls f(row of lane `src`, src) with the whole warp for every lane whose row
+// has more than a few new entries (a prompt); the other rows (one token, as a
+// rule) are left to their lanes.
+constexpr int kFewEntries = 4;
+template <typename F>
+__device__ __forceinline__ void for_wide_rows(const NewEntries& r, F f) {
+  unsigned m = __ballot_sync(0xffffffffu, r.e1 - r.e0 > kFewEntries);
+  while (m) {
+    const int src = __ffs(m) - 1;
+    m &= m - 1;
+    NewEntries w;
+    w.s = __shfl_sync(0xffffffffu, r.s, src);
+    w.e0 = __shfl_sync(0xffffffffu, r.e0, src);
+    w.e1 = __shfl_sync(0xffffffffu, r.e1, src);
+    f(w, src);
+  }
+}
+// How many of a row's new entries name no page, for each lane's row.
+__device__ __forceinline__ int count_missing(const KvTables& kv, const NewEntries& r) {
+  int k = 0;
+  if (r.e1 - r.e0 <= kFewEntries)
+    for (int e = r.e0; e < r.e1; ++e) k += kv.table[(int64_t)r.s * kv.max_pages + e] < 0;
+  for_wide_rows(r, [&](const NewEntries& w, int src) {
+    int c = 0;
+    for (int e = w.e0 + (threadIdx.x & 31); e < w.e1; e += 32)
+      c += kv.table[(int64_t)w.s * kv.max_pages + e] < 0;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == src) k = c;
+  });
+  return k;
+}
+
 // Sequences grow by add[i] tokens: entries of the new tokens that have no page
-// get one.  ws: the free list [n_pages].  short_pages: see the header.
+// get one.  A thread has a row.  ws: the free list [n_pages].  short_pages:
+// see the header.
 __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, const int32_t* slots,
                                                                const int32_t* add, int n,
                                                                int32_t* short_pages,
                                                                int32_t* ws) {
   __shared__ uint32_t used[kKvMaxSlots / 32];
   __shared__ int red[33];
+  const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   const int words = (kv.n_slots + 31) / 32;
@@ -74,22 +112,19 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
   // check everything and count the pages wanted
   bool bad = false;
   long long want = 0;
-  auto missing = [&](int s, int len, int more) {   // entries of the new tokens without a page
-    int k = 0;
-    const int e1 = (int)(((int64_t)len + more + kv.page_size - 1) / kv.page_size);
-    for (int e = (len + kv.page_size - 1) / kv.page_size; e < e1; ++e)
-      k += kv.table[(int64_t)s * kv.max_pages + e] < 0;
-    return k;
-  };
-  for (int i = threadIdx.x; i < n; i += kKvThreads) {
-    const int s = slots ? slots[i] : i, more = add[i];
-    if (!slot_ok(kv, s) || set_bit(used, s)) { bad = true; continue; }
-    const int len = slot_len(kv, s);
-    if (len < 0 || more < 0 || (int64_t)len + more > (int64_t)kv.max_pages * kv.page_size) {
-      bad = true;
-      continue;
+  for (int base = 0; base < n; base += kKvThreads) {
+    const int i = base + threadIdx.x;
+    NewEntries r{0, 0, 0};
+    if (i < n) {
+      const int s = slots ? slots[i] : i, more = add[i];
+      const int len = slot_ok(kv, s) && !set_bit(used, s) ? slot_len(kv, s) : -1;
+      if (len < 0 || more < 0 || (int64_t)len + more > (int64_t)kv.max_pages * kv.page_size)
+        bad = true;
+      else
+        r = NewEntries{s, (len + kv.page_size - 1) / kv.page_size,
+                       (len + more + kv.page_size - 1) / kv.page_size};
     }
-    want += missing(s, len, more);
+    want += count_missing(kv, r);
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
@@ -98,8 +133,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
     }
     return;
   }
-  int total;                                 // no table row wants over max_pages entries
-  block_exclusive_sum((int)min(want, (long long)(0x7fffffff / kKvThreads)), red, total);
+  // a thread's wish is held at the number of pages, so the sum cannot overflow
+  int total;
+  block_exclusive_sum((int)min(want, (long long)min(kv.n_pages, 0x7fffffff / kKvThreads)), red,
+                      total);
   const int got = list_free_pages(kv.refs, kv.n_pages, total, ws, red);
   if (got < total) {
     if (threadIdx.x == 0) {
@@ -111,26 +148,44 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
   int taken = 0;
   for (int base = 0; base < n; base += kKvThreads) {
     const int i = base + threadIdx.x;
-    int s = 0, len = 0, more = 0, k = 0;
+    NewEntries r{0, 0, 0};
+    int len = 0;
     if (i < n) {
-      s = slots ? slots[i] : i;
-      len = kv.lens[s];
-      more = add[i];
-      k = missing(s, len, more);
+      r.s = slots ? slots[i] : i;
+      const int old = kv.lens[r.s];
+      len = old + add[i];
+      r.e0 = (old + kv.page_size - 1) / kv.page_size;
+      r.e1 = (len + kv.page_size - 1) / kv.page_size;
     }
-    int sum, at = taken + block_exclusive_sum(k, red, sum);
-    if (i < n) {
-      const int e1 = (int)(((int64_t)len + more + kv.page_size - 1) / kv.page_size);
-      for (int e = (len + kv.page_size - 1) / kv.page_size; e < e1; ++e) {
-        int32_t* t = kv.table + (int64_t)s * kv.max_pages + e;
-        if (*t >= 0) continue;
-        const int page = ws[at++];
-        *t = page;
-        kv.refs[page] = 1;
-      }
-      kv.lens[s] = len + more;
+    if (total > 0) {
+      const int k = count_missing(kv, r);
+      int sum;
+      int at = taken + block_exclusive_sum(k, red, sum);
+      taken += sum;
+      for_wide_rows(r, [&](const NewEntries& w, int src) {
+        int to = __shfl_sync(0xffffffffu, at, src);
+        for (int e = w.e0; e < w.e1; e += 32) {
+          int32_t* t = kv.table + (int64_t)w.s * kv.max_pages + e + lane;
+          const bool take = e + lane < w.e1 && *t < 0;
+          const unsigned m = __ballot_sync(0xffffffffu, take);
+          if (take) {
+            const int page = ws[to + __popc(m & ((1u << lane) - 1))];
+            *t = page;
+            kv.refs[page] = 1;
+          }
+          to += __popc(m);
+        }
+      });
+      if (r.e1 - r.e0 <= kFewEntries)
+        for (int e = r.e0; e < r.e1; ++e) {
+          int32_t* t = kv.table + (int64_t)r.s * kv.max_pages + e;
+          if (*t >= 0) continue;
+          const int page = ws[at++];
+          *t = page;
+          kv.refs[page] = 1;
+        }
     }
-    taken += sum;
+    if (i < n) kv.lens[r.s] = len;
   }
   if (short_pages && threadIdx.x == 0) *short_pages = 0;
 }
@@ -365,11 +420,14 @@ struct KvAppendArgs {
   uint16_t* k_pages;
   uint16_t* v_pages;
   int64_t k_stride, v_stride;
-  int B, T, Hkv, head_chunks;                // 16-byte chunks per head
+  int B, T, Hkv;
 };
 
+template <int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int CH = D / 8;                  // 16-byte chunks per head
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= a.T) return;
@@ -409,11 +467,26 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a) {
   const uint4* vs = reinterpret_cast<const uint4*>(a.v + (int64_t)r * a.v_stride);
   uint4* kd = reinterpret_cast<uint4*>(a.k_pages);
   uint4* vd = reinterpret_cast<uint4*>(a.v_pages);
-  for (int x = lane; x < a.Hkv * a.head_chunks; x += 32) {
-    const int h = x / a.head_chunks, c = x % a.head_chunks;
-    const int64_t o = ((page * a.Hkv + h) * a.kv.page_size + row) * a.head_chunks + c;
-    kd[o] = ks[x];
-    vd[o] = vs[x];
+  // four chunks of the keys and four of the values on their way per lane
+  for (int x0 = lane; x0 < a.Hkv * CH; x0 += 128) {
+    uint4 kv4[4], vv4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = x0 + 32 * i;
+      if (x < a.Hkv * CH) {
+        kv4[i] = ks[x];
+        vv4[i] = vs[x];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = x0 + 32 * i;
+      if (x < a.Hkv * CH) {
+        const int64_t o = ((page * a.Hkv + x / CH) * a.kv.page_size + row) * CH + x % CH;
+        kd[o] = kv4[i];
+        vd[o] = vv4[i];
+      }
+    }
   }
 }
 
