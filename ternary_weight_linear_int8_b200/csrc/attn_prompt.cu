@@ -316,30 +316,46 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
 //
 // The tile kernel: 2 x 128 rows per CTA on tcgen05.  Twenty warps:
 //   * 16 softmax warps, 8 for each 128 rows: a thread has one row (a TMEM
-//     lane) and half of a key tile's columns, so four of them share a
-//     scheduler and hide each other's latencies;
+//     lane) and half of a step's columns, so four of them share a scheduler
+//     and hide each other's latencies;
 //   * warp 16 (one thread): TMA loads of Q once and of K, V tiles of 128 keys
 //     into a ring;
 //   * warp 17 (one thread): the MMAs.
-// Per key tile j and row half i:
-//   S_i = Q_i K_j^T   both operands in shared memory, fp32 scores in TMEM
+// Per step of 64 keys and row half i:
+//   S_i = Q_i K^T    both operands in shared memory, fp32 scores in one of two
+//                    buffers in TMEM
 //   P_i = exp2(c S_i - m_i)   read by the softmax threads, written back over
-//                             S_i as bf16 pairs (64 of its 128 columns)
-//   O_i += P_i V_j    P_i from TMEM, V_j (rows of D values, so MN-major) from
-//                     shared memory, fp32 sums in TMEM
-// The halves alternate: while one half's scores are in the softmax the tensor
-// cores run the other half's two products.  MMAs are executed in
-// issue order, so S_i of tile j + 1 may overwrite P_i as soon as it is issued
-// after O_i += P_i V_j, and its completion says that O_i is up to date.
+//                    the scores as bf16 pairs (32 of their 64 columns)
+//   O_i += P_i V     P_i from TMEM, V (rows of D values, so MN-major) from
+//                    shared memory, fp32 sums in TMEM
+// The scores of a half are two steps ahead of its outputs, so the softmax
+// warps find the next scores when they have done with the last.  MMAs are
+// executed in issue order: the scores of step u + 2 may overwrite P of step u
+// as soon as they are issued after its product.
 //
 // The reference m_i of a row only has to keep the exponentials in range, not
 // to be the running maximum: the result is divided by the same scaled sum.  So
-// a tile's exponentials are taken with the reference of the tiles before it
+// a step's exponentials are taken with the reference of the steps before it
 // while its own maximum is still being found, and only if a row outgrows its
-// reference by 2^8 (always in the first tile) is the tile done again, with
+// reference by 2^8 (always in the first step) is the step done again, with
 // O_i rescaled.  bf16 has fp32's range, so probabilities up to 2^8 lose
 // nothing.
-constexpr int kPtKeys = 128;
+//
+// Measured (device time): 4096 tokens of 20 heads of 128 on 4 key-value heads
+// 99 us (865 TFLOP/s), 16384 tokens 1.21 ms (1138, power capped), 4096 tokens of
+// 16 heads of 64 66 us.  With D = 128 the bound is shared memory: a score MMA
+// reads Q and K at the full 128 bytes a clock (8 x 6 KB per half and step),
+// the output MMAs read V at half of it, and the ring's TMA writes come on
+// top; the MMAs alone, with no softmax, take 1650 cycles a step of 1239 that
+// they take without the ring's traffic.  With D = 64 it is the exponentials
+// (16 a clock and SM).  Alternatives: scores 128 keys wide and single buffered
+// (less shared-memory traffic, but softmax and MMAs of a half in turn): 97 us,
+// 1.18 ms and 72 us; one thread per whole row (8 softmax warps): 105 us and
+// more; two issuing warps, one per half (the halves fall into step and wait
+// for the same unit): 108 us; a quarter of the exponentials as polynomials on
+// the fp32 pipe: 104 us, 1.28 ms and 70 us (the longer instruction stream
+// costs more than the special function unit saves).
+constexpr int kPtKeys = 128, kPtSub = 64;
 constexpr int kPtThreads = 640;
 constexpr int kPtRegs = 96;                  // 65536 / 640, in steps of 8
 constexpr int kPtRegsSoftmax = 104, kPtRegsIssue = 64;
@@ -351,12 +367,12 @@ struct PtCfg {
   static constexpr int kBlock = 128 * 128;                // 128 rows of 64 bf16
   static constexpr int kTile = kHalves * kBlock;          // a Q half, K or V tile
   static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kBars = 2 * kStages + 8;
+  static constexpr int kBars = 2 * kStages + 14;
   static constexpr int kExch = 2 * 2 * 128 * 4;           // a float per softmax thread
   static constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + kExch + kBars * 8 + 64;
-  // D fp32, A and B bf16, M 128; scores: N 128, both K-major; outputs: N = D, B MN-major
+  // D fp32, A and B bf16, M 128; scores: N 64, both K-major; outputs: N = D, B MN-major
   static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) |
-                                      ((uint32_t)(kPtKeys >> 3) << 17) | (8u << 24);
+                                      ((uint32_t)(kPtSub >> 3) << 17) | (8u << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
                                       ((uint32_t)(D >> 3) << 17) | (8u << 24);
 };
@@ -443,6 +459,15 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* 
       "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
 // Waits for this thread's loads; the 32 registers pass through it, so no use
 // of them can be scheduled before the wait.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
@@ -492,37 +517,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 2^x of a pair on the fp32 pipe, for -inf <= x < 128: n = x rounded to an
-// integer (by adding 1.5 * 2^23), 2^(x - n) by a polynomial whose constant term
-// is 1 and whose other coefficients minimise the largest relative error on
-// [-1/2, 1/2] (weighted least squares with Lawson's weights; 1.1e-7, below
-// the hardware approximation's 2 ulp), n added to the exponent field.  x is
-// held at -127, where the field becomes 0: masked scores give exactly 0.
-__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
-  float a, b;
-  f2_unpack(x, a, b);
-  x = f2_pack(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
-  const uint64_t big = f2_pack(12582912.0f, 12582912.0f), neg = f2_pack(-12582912.0f, -12582912.0f);
-  const uint64_t t = f2_add(x, big), n = f2_add(t, neg);
-  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
-  uint64_t p = f2_fma(f, f2_pack(0.0013264727f, 0.0013264727f), f2_pack(0.009671513f, 0.009671513f));
-  p = f2_fma(p, f, f2_pack(0.055507336f, 0.055507336f));
-  p = f2_fma(p, f, f2_pack(0.24022242f, 0.24022242f));
-  p = f2_fma(p, f, f2_pack(0.693147f, 0.693147f));
-  p = f2_fma(p, f, f2_pack(1.0f, 1.0f));
-  float pa, pb, ta, tb;
-  f2_unpack(p, pa, pb);
-  f2_unpack(t, ta, tb);
-  return f2_pack(__int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23)),
-                 __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23)));
-}
-// Of every eight pairs of scores so many take ex2_pair, the others the special
-// function unit (4 exponentials per clock and scheduler, which alone would
-// take as long as the tensor cores' products).  4096-token prefill of 20 heads
-// with 0 / 2 / 3 / 4 of 8: 97.9 / 95.4 / 95.8 / 106 us; 16384 tokens: 1230 /
-// 1138 / 1186 / 1354.
-constexpr int kPtEmulated = 2;
-
 template <int D>
 __global__ void __launch_bounds__(kPtThreads, 1)
     prompt_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -535,9 +529,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(exch + C::kExch / 4);
   uint64_t* kv_empty = kv_full + S;
   uint64_t* q_full = kv_empty + S;
-  uint64_t* s_full = q_full + 1;             // [2]
-  uint64_t* p_full = s_full + 2;             // [2]
-  uint64_t* o_full = p_full + 2;             // [2]
+  uint64_t* s_full = q_full + 1;             // [2 halves][2 buffers]
+  uint64_t* p_full = s_full + 4;             // [2][2]
+  uint64_t* o_done = p_full + 4;             // [2] after every step
+  uint64_t* o_full = o_done + 2;             // [2] after the last one
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_full + C::kBars);
   PromptTile* s_tile = reinterpret_cast<PromptTile*>(tmem_slot + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -549,9 +544,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(&kv_empty[s], 1);
     }
     mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&o_done[i], 1);
       mbar_init(&o_full[i], 1);
     }
     fence_mbar_init();
@@ -584,19 +582,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const uint32_t tmem = *tmem_slot;
   if (tid == 0) pdl_launch_dependents();
 
-  // the two halves: tokens and key tiles
+  // the two halves: tokens and steps of 64 keys
   const int half_tokens = a.half_tokens;
   const int end = min(t.t0 + a.tile_tokens, t.ql);         // the tile may be one half long
   const int shift = t.kl - t.ql;             // row r sees keys 0 .. r + shift
-  int n_tiles[2];
+  int n_steps[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int first = t.t0 + i * half_tokens;
     const int last = min(first + half_tokens, end) - 1;
     const int keys = last < first ? 0 : max(0, min(t.kl, last + shift + 1));
-    n_tiles[i] = (keys + kPtKeys - 1) / kPtKeys;
+    n_steps[i] = (keys + kPtSub - 1) / kPtSub;
   }
-  const int n_all = max(n_tiles[0], n_tiles[1]);
+  const int n_all = max(n_steps[0], n_steps[1]);
 
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsIssue));
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                       h * 64, kvh * a.group, t.q0 + t.t0 + i * half_tokens);
       bool ok = true;
       int u = 0;                             // tiles K_0 V_0 K_1 V_1 ...
-      for (; u < 2 * n_all; ++u) {
+      for (; u < 2 * ((n_all + 1) / 2); ++u) {
         const int s = u % S;
         if (u >= S && !mbar_wait(&kv_empty[s], ((u / S) - 1) & 1)) { ok = false; break; }
         mbar_arrive_expect_tx(&kv_full[s], (uint32_t)C::kTile);
@@ -627,59 +625,64 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // -------------------------------------------------------- MMA issuer
       const uint64_t q_desc = sw128_desc(smem_u32(smem)), k_desc = sw128_desc(smem_u32(ring));
       const uint64_t v_desc = sw128_mn_desc(smem_u32(ring), C::kBlock);
-      auto scores = [&](int i, int s) {      // S_i = Q_i K^T, K in stage s
+      // S_i[u & 1] = Q_i K^T for step u, its 64 keys in stage s
+      auto scores = [&](int i, int u, int s) {
+        const uint32_t st = tmem + (uint32_t)(i * 128 + (u & 1) * kPtSub);
         const uint64_t qd = q_desc + (uint64_t)(i * (C::kTile >> 4));
-        const uint64_t kd = k_desc + (uint64_t)(s * (C::kTile >> 4));
+        const uint64_t kd = k_desc + (uint64_t)(s * (C::kTile >> 4) + (u & 1) * (kPtSub * 128 >> 4));
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t o = (uint64_t)((x >> 2) * (C::kBlock >> 4) + 2 * (x & 3));
-          tc_mma_bf16(tmem + (uint32_t)(i * kPtKeys), qd + o, kd + o, C::kIdescS, x > 0);
+          tc_mma_bf16(st, qd + o, kd + o, C::kIdescS, x > 0);
         }
-        tc_commit(&s_full[i]);
+        tc_commit(&s_full[2 * i + (u & 1)]);
       };
-      auto outputs = [&](int i, int s, bool add) {   // O_i (+)= P_i V, V in stage s
-        const uint64_t vd = v_desc + (uint64_t)(s * (C::kTile >> 4));
-        const uint32_t ot = tmem + (uint32_t)(2 * kPtKeys + i * D), pt = tmem + (uint32_t)(i * kPtKeys);
-        tc_mma_bf16_ts(ot, pt, vd, C::kIdescO, add);
+      // O_i (+)= P_i[u & 1] V for step u, its 64 values in stage s
+      auto outputs = [&](int i, int u, int s) {
+        const uint64_t vd = v_desc + (uint64_t)(s * (C::kTile >> 4) + (u & 1) * (kPtSub * 128 >> 4));
+        const uint32_t ot = tmem + (uint32_t)(256 + i * D);
+        const uint32_t pt = tmem + (uint32_t)(i * 128 + (u & 1) * kPtSub);
+        tc_mma_bf16_ts(ot, pt, vd, C::kIdescO, u > 0);
 #pragma unroll
-        for (int x = 1; x < kPtKeys / 16; ++x)
+        for (int x = 1; x < kPtSub / 16; ++x)
           tc_mma_bf16_ts(ot, pt + 8 * x, vd + x * (2048 >> 4), C::kIdescO, 1);
+        tc_commit(&o_done[i]);
+        if (u + 1 == n_steps[i]) tc_commit(&o_full[i]);
       };
-      int s = 1;                             // stage and phase of V_j
-      uint32_t ph = 0;
+      // scores run two steps ahead of the outputs; K of tile j and V of tile j
+      // are ring entries 2 j and 2 j + 1
       bool ok = mbar_wait(q_full, 0) && mbar_wait(&kv_full[0], 0);
       if (ok) {
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (n_tiles[i] > 0) scores(i, 0);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (u < n_steps[i]) scores(i, u, 0);
         tc_commit(&kv_empty[0]);
       }
-      for (int j = 0; j < n_all && ok; ++j) {
-        const int sk = s + 1 == S ? 0 : s + 1;               // K_{j+1}
+      int s = 1;                             // stage and phase of the step's V
+      uint32_t ph = 0;
+      for (int u = 0; u < n_all && ok; ++u) {
+        const int sk = s + 1 == S ? 0 : s + 1;               // K of step u + 2
         const uint32_t phk = s + 1 == S ? ph ^ 1 : ph;
-        const bool more = j + 1 < n_all;
-        ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk));
+        const bool more = u + 2 < n_all;
+        if (!(u & 1)) ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          // one half's two products, then the other's: the halves fall into
-          // step with one in the softmax while the other is here
-          if (!ok || j >= n_tiles[i]) continue;
-          ok = mbar_wait(&p_full[i], (uint32_t)(j & 1));
+          if (!ok || u >= n_steps[i]) continue;
+          ok = mbar_wait(&p_full[2 * i + (u & 1)], (uint32_t)((u >> 1) & 1));
           if (!ok) continue;
           tc_fence_after();
-          outputs(i, s, j > 0);
-          if (j + 1 < n_tiles[i])
-            scores(i, sk);
-          else
-            tc_commit(&o_full[i]);
+          outputs(i, u, s);
+          if (u + 2 < n_steps[i]) scores(i, u + 2, sk);
         }
-        if (ok) {
-          tc_commit(&kv_empty[s]);
-          if (more) tc_commit(&kv_empty[sk]);
+        if (ok && ((u & 1) || u + 1 == n_all)) tc_commit(&kv_empty[s]);
+        if (ok && more && ((u & 1) || u + 3 == n_all)) tc_commit(&kv_empty[sk]);
+        if (u & 1) {
+          s = sk + 1 == S ? 0 : sk + 1;
+          ph = sk + 1 == S ? phk ^ 1 : phk;
         }
-        s = sk + 1 == S ? 0 : sk + 1;
-        ph = sk + 1 == S ? phk ^ 1 : phk;
       }
     }
     __syncwarp();
@@ -690,15 +693,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int r = 32 * (warp & 3) + lane;    // this thread's row
     const int pair = 1 + 4 * i + (warp & 3);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t st = tmem + lanes + (uint32_t)(i * kPtKeys + cg * 64);
-    const uint32_t pt = tmem + lanes + (uint32_t)(i * kPtKeys + cg * 32);
-    const uint32_t ot = tmem + lanes + (uint32_t)(2 * kPtKeys + i * D + cg * (D / 2));
+    const uint32_t st = tmem + lanes + (uint32_t)(i * 128 + cg * 32);
+    const uint32_t pt = tmem + lanes + (uint32_t)(i * 128 + cg * 16);
+    const uint32_t ot = tmem + lanes + (uint32_t)(256 + i * D + cg * (D / 2));
     float* mine = exch + (2 * i + cg) * 128 + r;
     const float* other = exch + (2 * i + (cg ^ 1)) * 128 + r;
-    const int n = i ? n_tiles[1] : n_tiles[0];
+    const int n = i ? n_steps[1] : n_steps[0];
     const int first = t.t0 + i * half_tokens;
     const int token = first + r / a.group;
-    const int lim = token + shift - cg * 64; // last key the row sees, from this column half
+    const int lim = token + shift - cg * 32; // last key the row sees, from this column half
     const float c = a.scale_log2;
     const uint64_t c2 = f2_pack(c, c);
     const float slack = 8.0f / c;
@@ -708,39 +711,35 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // the same barriers (without further waits) and nothing is written
     bool ok = true, poison = false;
     for (int j = 0; j < n; ++j) {
-      if (ok) ok = mbar_wait(&s_full[i], (uint32_t)(j & 1));
+      const int buf = 2 * i + (j & 1);
+      const uint32_t sub = (uint32_t)((j & 1) * kPtSub);
+      if (ok) ok = mbar_wait(&s_full[buf], (uint32_t)((j >> 1) & 1));
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const bool border = j * kPtKeys + kPtKeys - 1 > first + shift;   // some row ends inside
-      const int e = lim - j * kPtKeys;
+      const bool border = j * kPtSub + kPtSub - 1 > first + shift;   // some row ends inside
+      const int e = lim - j * kPtSub;
       while (true) {
         const float neg = m == -INFINITY ? 0.0f : -m * c;
         const uint64_t neg2 = f2_pack(neg, neg);
-        uint32_t s[64], p[32];
+        uint32_t s[32], p[16];
         float mx[2] = {-INFINITY, -INFINITY};
         uint64_t t2[2] = {0, 0};
-        tmem_ld32_async(st, s);
-        tmem_ld32_async(st + 32, s + 32);
+        tmem_ld32_async(st + sub, s);
         tmem_wait_ld(s);
-        tmem_wait_ld(s + 32);
         if (border) {
 #pragma unroll
-          for (int x = 0; x < 64; ++x)
+          for (int x = 0; x < 32; ++x)
             if (x > e) s[x] = 0xff800000u;
         }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
+        for (int x = 0; x < 16; ++x) {
           const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
           mx[x & 1] = max3_nan(mx[x & 1], s0, s1);
           const uint64_t y = f2_fma(f2_pack(s0, s1), c2, neg2);
           float e0, e1;
-          if ((x * kPtEmulated) % 8 < kPtEmulated) {
-            f2_unpack(ex2_pair(y), e0, e1);
-          } else {
-            f2_unpack(y, e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-          }
+          f2_unpack(y, e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
           p[x] = pack_bf16(e0, e1);
           t2[x & 1] = f2_add(t2[x & 1], f2_pack(e0, e1));
         }
@@ -756,6 +755,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const float f = to == m ? 1.0f : ex2((m - to) * c);
           m = to;
           if (j > 0) {
+            // O holds the steps before this one once their MMAs are done
+            // (these scores came after those of step j - 2, so the wait can
+            // only be for step j - 1 and its parity is enough)
+            if (ok) ok = mbar_wait(&o_done[i], (uint32_t)((j - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
             const uint64_t f2 = f2_pack(f, f);
             l2[0] = f2_fma(l2[0], f2, 0);
             l2[1] = f2_fma(l2[1], f2, 0);
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           continue;
         }
         poison |= !(top < INFINITY);
-        tmem_st32_async(pt, p);
+        tmem_st16_async(pt + sub, p);
         l2[0] = f2_add(l2[0], t2[0]);
         l2[1] = f2_add(l2[1], t2[1]);
         break;
@@ -780,7 +785,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
+      if (lane == 0) mbar_arrive(&p_full[buf]);
     }
     // ------------------------------------------------------------ epilogue
     float l, l1;

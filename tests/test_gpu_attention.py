@@ -105,6 +105,89 @@ def test_prompt_matches_definition(heads, ql, kl):
     run_prompt(q, k, v, cq, ck)
 
 
+# long enough on average (over 256 keys a sequence) for the tensor-core kernel: tiles of one and of two halves, borders
+# inside and at the ends of steps, groups that do not divide 128, sequences that are empty or see nothing
+TILES = [
+    ((20, 4, 128), [257], None),
+    ((20, 4, 128), [1200, 0, 1, 130], None),
+    ((4, 4, 64), [320, 319, 321], None),
+    ((2, 1, 128), [255, 256, 257, 640], None),
+    ((7, 1, 64), [700], None),
+    ((12, 4, 128), [100, 3], [1000, 3]),
+    ((16, 1, 64), [5, 40], [700, 40]),
+    ((64, 1, 128), [19], [583]),
+    ((33, 1, 64), [30, 2], [30, 1130]),
+    ((48, 1, 128), [9, 1], [901, 64]),
+    ((3, 3, 128), [513], None),
+    ((8, 2, 128), [700, 10, 5], [900, 0, 1]),
+    ((8, 2, 64), [900, 2], [600, 1]),                # the first 300 rows see nothing
+    ((8, 2, 128), [600], [300]),                     # whole tiles see nothing
+    ((10, 2, 128), [1, 1, 1, 1], [640, 128, 129, 1024]),
+    ((64, 8, 128), [1000, 300], None),
+    ((64, 8, 64), [129, 1], [1025, 500]),
+]
+
+
+def some_rows(ql):
+    """Rows at the borders of tiles and halves of any group, and a few others."""
+    keep = set()
+    for n in ql:
+        for at in (0, 2, 3, 8, 16, 25, 32, 50, 64, 127, 128, 250, 255, 256, 300, 512, n // 2, n):
+            keep |= {at - 1, at, at + 1}
+    return keep
+
+
+@pytest.mark.parametrize("heads,ql,kl", TILES)
+def test_prompt_tiles_match_definition(heads, ql, kl):
+    Hq, Hkv, D = heads
+    kl = ql if kl is None else kl
+    assert sum(kl) > 256 * len(kl)
+    rng = np.random.default_rng(sum(ql) * 5 + Hq + D)
+    cq, ck = cu(ql), cu(kl)
+    q, k, v = rand(rng, cq[-1], Hq, D, scale=2.0), rand(rng, ck[-1], Hkv, D, scale=1.5), rand(rng, ck[-1], Hkv, D)
+    run_prompt(q, k, v, cq, ck, rows=some_rows(ql))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_tiles_leave_what_is_outside(D):
+    rng = np.random.default_rng(D + 1)
+    Hq, Hkv, ql, kl = 10, 2, [310, 0, 9], [900, 0, 9]
+    cq, ck = cu(ql, first=5), cu(kl, first=3)
+    q, k, v = rand(rng, cq[-1] + 40, Hq, D), rand(rng, ck[-1] + 150, Hkv, D), rand(rng, ck[-1] + 150, Hkv, D)
+    for t, c in ((q, cq), (k, ck), (v, ck)):
+        t[:c[0]] = NAN
+        t[c[-1]:] = INF
+    run_prompt(q, k, v, cq, ck, rows=some_rows(ql))
+
+
+@pytest.mark.parametrize("D,bad", [(64, NAN), (128, NAN), (128, INF), (64, -INF)])
+@pytest.mark.parametrize("where", ["v", "k", "q"])
+def test_prompt_tiles_poison(D, bad, where):
+    rng = np.random.default_rng(31)
+    Hq, Hkv, n = 4, 2, 500
+    q, k, v = rand(rng, n, Hq, D).abs(), rand(rng, n, Hkv, D), rand(rng, n, Hkv, D)
+    dict(q=q, k=k, v=v)[where][397, 1, 5] = bad
+    run_prompt(q, k, v, [0, n], [0, n], lse=where == "v", rows={0, 1, 255, 300, 383, 384, 395, 396, 397, 398, 420, 499})
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_tiles_extreme_scores(D):
+    rng = np.random.default_rng(32)
+    n, low = 520, torch.finfo(BF).min
+    rows = {0, 1, 63, 64, 65, 130, 255, 256, 400, 519}
+    q, k, v = rand(rng, n, 2, D).abs() + 0.5, rand(rng, n, 1, D), rand(rng, n, 1, D)
+    k[3::5] = low
+    run_prompt(q, k, v, [0, n], [0, n], lse=False, rows=rows)
+    k[:] = low
+    y, lse = B.bitnet_attn_prompt(q.cuda(), k.cuda(), v.cuda(), i32([0, n]), want_lse=True)
+    assert bool((y == 0).all()) and bool((lse == -INF).all())
+    run_prompt(q * 8, rand(rng, n, 1, D, scale=40.0), v, [0, n], [0, n], rows=rows)
+    # scores that grow by more than the reference's slack at every step, and ones that only fall
+    for sign in (1, -1):
+        ramp = (sign * torch.arange(n, dtype=torch.float32)[:, None, None] * 0.05).expand(n, 1, D).to(BF)
+        run_prompt(torch.ones(n, 5, D, dtype=BF), ramp, v, [0, n], [0, n], rows=rows)
+
+
 @pytest.mark.parametrize("heads,ql,kl", [((20, 4, 128), [1500], [1500]), ((16, 16, 64), [700, 300], [2500, 300]),
                                          ((64, 8, 128), [1100, 900], [1100, 900])])
 def test_prompt_long_sampled_rows(heads, ql, kl):
@@ -197,6 +280,31 @@ def test_prompt_bad_bounds_are_recorded():
     assert B.bitnet_last_device_status() == 1
     out.check()
     assert torch.equal(out.t[:20], good[:20])           # the sound sequence is computed
+
+
+def test_prompt_captured_and_replayed_on_new_bounds():
+    """A captured call reads the bounds at replay."""
+    rng = np.random.default_rng(33)
+    T, Hq, Hkv, D = 900, 10, 2, 128
+    q, k, v = rand(rng, T, Hq, D), rand(rng, T, Hkv, D), rand(rng, T, Hkv, D)
+    qd, kd, vd, c = q.cuda(), k.cuda(), v.cuda(), i32([0, 400, 900])
+    y = torch.zeros_like(qd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        B.bitnet_attn_prompt(qd, kd, vd, c, y=y)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        B.bitnet_attn_prompt(qd, kd, vd, c, y=y)
+    for bounds in ([0, 700, 899], [3, 3, 500]):
+        c.copy_(i32(bounds))
+        y.fill_(9.0)
+        graph.replay()
+        yh = y.double().cpu().numpy()
+        for t, h, *want in A.prompt(f64(q), f64(k), f64(v), bounds, bounds, D ** -0.5, rows={0, 60, 399, -1, -2}):
+            check_row(yh[t, h], None, want, (t, h))
+        assert bool((y[:bounds[0]] == 9).all()) and bool((y[bounds[-1]:] == 9).all())
 
 
 def test_prompt_same_bits_again_on_another_stream():
