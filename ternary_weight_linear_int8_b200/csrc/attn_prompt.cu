@@ -557,30 +557,34 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
-  pdl_wait();
-  if (warp == 0) {
-    const PromptTile f = prompt_find_tile(a, blockIdx.x / a.Hkv, blockIdx.x == 0);
-    if (lane == 0) *s_tile = f;
-  }
-  __syncthreads();
-  const PromptTile t = *s_tile;
-  if (!t.ok) return;
   if (smem_u32(smem) & 1023u) {              // the swizzle counts on it
     if (tid == 0) record_error(BITNET_ERR_UNSUPPORTED);
     return;
   }
-  if (warp == 17) {
+  if (warp == 0) {
+    pdl_wait();
+    const PromptTile f = prompt_find_tile(a, blockIdx.x / a.Hkv, blockIdx.x == 0);
+    if (lane == 0) *s_tile = f;
+  } else if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
                  "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const PromptTile t = *s_tile;
   if (tid == 0) pdl_launch_dependents();
+  if (!t.ok) {
+    if (warp == 17)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                   : "memory");
+    return;
+  }
 
   // the two halves: tokens and steps of 64 keys
   const int half_tokens = a.half_tokens;
@@ -836,11 +840,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncwarp();
     const int r0 = 32 * (warp & 3);
     if (ok) {
-#pragma unroll 4
-      for (int x = lane; x < 32 * CH; x += 32) {
-        const int rr = x / CH, ch = x % CH, row = r0 + rr;
+      const uint32_t inv_group = (65536u + (uint32_t)a.group - 1) / (uint32_t)a.group;
+#pragma unroll
+      for (int y = 0; y < CH; ++y) {
+        const int x = y * 32 + lane, rr = x / CH, ch = x % CH, row = r0 + rr;
         if (row < rows) {
-          const int tok = row / a.group, head = kvh * a.group + row % a.group;
+          // row / group, exact for rows below 128 and groups up to 64
+          const int tok = (int)(((uint32_t)row * inv_group) >> 16);
+          const int head = kvh * a.group + row - tok * a.group;
           *reinterpret_cast<uint4*>(a.y + (int64_t)(t.q0 + first + tok) * a.y_stride +
                                     (int64_t)head * D + cg * (D / 2) + ch * 8) = lds_v4(at(rr, ch));
         }

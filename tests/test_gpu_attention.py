@@ -225,6 +225,16 @@ def test_prompt_poison_behind_the_causal_border(D, bad, where):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("where,bad", [("v", NAN), ("v", -INF), ("k", NAN), ("q", INF)])
+def test_short_prompt_poison(D, where, bad):
+    rng = np.random.default_rng(34)
+    Hq, Hkv, n = 4, 2, 70
+    q, k, v = rand(rng, n, Hq, D).abs(), rand(rng, n, Hkv, D), rand(rng, n, Hkv, D)
+    dict(q=q, k=k, v=v)[where][45, 1, 5] = bad
+    run_prompt(q, k, v, [0, n], [0, n], lse=where == "v")
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_prompt_extreme_scores(D):
     """Keys of the type's lowest value (scores far below the rest, or overflowing to -inf for every key of a row)."""
     rng = np.random.default_rng(4)
