@@ -832,15 +832,14 @@ def bitnet_kv_copy_pages(k_pages, v_pages, pairs: torch.Tensor, n_pairs: torch.T
     L = len(k_pages)
     if len(v_pages) != L or not L:
         raise ValueError("k_pages and v_pages must be non-empty lists of equal length")
-    shape, dev = k_pages[0].shape, n_pairs.get_device()
-    if len(shape) != 4:
-        raise ValueError("pages must be [n_pages, heads, page_size, D]")
-    ptrs = []
+    first, dev = k_pages[0], n_pairs.get_device()
+    if first.dim() != 4 or first.dtype not in _BITS16:
+        raise ValueError("pages must be [n_pages, heads, page_size, D] with 16-bit elements")
+    n, nbytes, ptrs = first.shape[0], first.nbytes, []
     for ts in (k_pages, v_pages):
         for t in ts:
-            if t.shape != shape or t.get_device() != dev or t.dtype not in _BITS16 or \
-                    not t.is_contiguous():
-                raise ValueError("all pages must be contiguous 16-bit CUDA tensors of one shape")
+            if t.nbytes != nbytes or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("all pages must be contiguous CUDA tensors of one size")
             ptrs.append(t.data_ptr())
     np_ = _index(n_pairs, "n_pairs", dev, 1)
     if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or \
@@ -848,8 +847,7 @@ def bitnet_kv_copy_pages(k_pages, v_pages, pairs: torch.Tensor, n_pairs: torch.T
         raise ValueError("pairs must be a contiguous [n, 2] int32 tensor")
     both = (ctypes.c_void_p * (2 * L))(*ptrs)
     at = ctypes.addressof(both)
-    n, h, s, d = shape
-    _run("bitnet_kv_copy_pages", dev, L, at, at + 8 * L, n, h * s * d * 2, pairs.data_ptr(), np_,
+    _run("bitnet_kv_copy_pages", dev, L, at, at + 8 * L, n, nbytes // n, pairs.data_ptr(), np_,
          min(pairs.shape[0], n))
 
 

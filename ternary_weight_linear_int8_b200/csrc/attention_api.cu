@@ -350,9 +350,11 @@ bitnet_status bitnet_kv_fork(const bitnet_kv_tables* kv, const int32_t* parents,
   const KvTables t = device_tables(kv);
   int32_t* ws = static_cast<int32_t*>(workspace);
   cudaStream_t s = as_stream(stream);
+  const bool one_block = n * kv->max_pages <= kKvOneBlock;
   if (launch_pdl(kv_fork_plan_kernel, 1, kKvThreads, 0, s, t, parents, children, (int)n, pairs,
-                 n_pairs, short_pages, ws) != cudaSuccess)
+                 n_pairs, short_pages, ws, one_block) != cudaSuccess)
     return BITNET_ERR_CUDA;
+  if (one_block) return BITNET_OK;
   return launch_pdl(kv_fork_rows_kernel, kv_blocks(n * kv->max_pages, d.num_sms), 256, 0, s, t,
                     parents, children, (int)n, (const int32_t*)ws) == cudaSuccess
              ? BITNET_OK : BITNET_ERR_CUDA;
@@ -389,9 +391,11 @@ bitnet_status bitnet_kv_compact(const bitnet_kv_tables* kv, int32_t* pairs, int3
   const KvTables t = device_tables(kv);
   int32_t* ws = static_cast<int32_t*>(workspace);
   cudaStream_t s = as_stream(stream);
-  if (launch_pdl(kv_compact_plan_kernel, 1, kKvThreads, 0, s, t, pairs, n_pairs, live, ws) !=
-      cudaSuccess)
+  const bool one_block = kv->n_slots * kv->max_pages <= kKvOneBlock;
+  if (launch_pdl(kv_compact_plan_kernel, 1, kKvThreads, 0, s, t, pairs, n_pairs, live, ws,
+                 one_block) != cudaSuccess)
     return BITNET_ERR_CUDA;
+  if (one_block) return BITNET_OK;
   return launch_pdl(kv_compact_table_kernel, kv_blocks(kv->n_slots * kv->max_pages, d.num_sms), 256,
                     0, s, t, (const int32_t*)ws) == cudaSuccess
              ? BITNET_OK : BITNET_ERR_CUDA;
