@@ -582,7 +582,7 @@ def bitnet_ffn_tp_finish(acc, I, gamma_down, amax2, sumsq_x, sumsq_h, eps=1e-5, 
 # These calls take a few microseconds on the device, so their marshalling is
 # kept short: device ordinals instead of device objects, the raw stream handle
 # instead of a stream object.
-_BITS16 = (torch.bfloat16, torch.int16, torch.float16, torch.uint16)
+_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 

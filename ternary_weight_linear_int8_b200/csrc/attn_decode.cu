@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnDecodeArgs a, 
   const int b = (int)(id / a.Hq), head = (int)(id % a.Hq);
   uint16_t* yr = a.y + (int64_t)b * a.y_stride + (int64_t)head * D + lane * V;
   const long long W = a.first_unit[a.B], at = a.first_unit[b], to = a.first_unit[b + 1];
-  const int chunks = (int)(to - at) / (a.Hkv * a.hb);
+  const int chunks = (int)((to - at) / ((long long)a.Hkv * a.hb));
   if (chunks == 0) {
     if (part == 0) {
 #pragma unroll

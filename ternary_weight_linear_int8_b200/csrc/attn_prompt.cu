@@ -72,8 +72,9 @@ __device__ __forceinline__ PromptTile prompt_find_tile(const AttnPromptArgs& a, 
       t.kl = __shfl_sync(0xffffffffu, k1 - k0, src);
       const int ns = __shfl_sync(0xffffffffu, n, src);
       const int first = seen + __shfl_sync(0xffffffffu, inc, src) - ns;
-      t.t0 = (ns - 1 - (x - first)) * a.tile_tokens;
-      t.ok = 1;
+      const int at = x - first;              // outside [0, ns) only if bad bounds overflow the count
+      t.t0 = (ns - 1 - at) * a.tile_tokens;
+      t.ok = at >= 0 && at < ns;
       if (!record) return t;
       x = 0x7fffffff;                        // go on for the checks alone
     }
@@ -85,7 +86,8 @@ __device__ __forceinline__ PromptTile prompt_find_tile(const AttnPromptArgs& a, 
 // One row by one warp in fp32 with the masked keys skipped: 32 keys at a time,
 // one per lane for the scores, then one output column set per lane.  For rows
 // whose tiled result is not finite: there a masked probability (0) times a
-// value that is infinite or NaN gives NaN, and this gives the row's own value.
+// value of the same sequence that is infinite or NaN gives NaN, and this gives
+// the row's own value.
 template <int D>
 __device__ __noinline__ void prompt_row_by_warp(const AttnPromptArgs& a, const PromptTile& t,
                                                 int token, int head) {
@@ -533,6 +535,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   uint64_t* p_full = s_full + 4;             // [2][2]
   uint64_t* o_done = p_full + 4;             // [2] after every step
   uint64_t* o_full = o_done + 2;             // [2] after the last one
+  uint64_t* v_clean = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_full + C::kBars);
   PromptTile* s_tile = reinterpret_cast<PromptTile*>(tmem_slot + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -544,6 +547,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(&kv_empty[s], 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(v_clean, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
@@ -599,32 +603,53 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     n_steps[i] = (keys + kPtSub - 1) / kPtSub;
   }
   const int n_all = max(n_steps[0], n_steps[1]);
+  // the last tile of values reaches behind the sequence
+  const int last_tile = (n_all - 1) >> 1;
+  const bool v_tail = n_all > 0 && (last_tile + 1) * kPtKeys > t.kl;
 
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsIssue));
-    if (warp == 16 && elect_one() && n_all > 0) {
+    if (warp == 16 && n_all > 0) {
       // ------------------------------------------------------ TMA producer
-      mbar_arrive_expect_tx(q_full, (uint32_t)(2 * C::kHalves * half_tokens * a.group * 128));
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tma_load_3d(smem_u32(smem) + (uint32_t)(i * C::kTile + h * C::kBlock), &tq, q_full,
-                      h * 64, kvh * a.group, t.q0 + t.t0 + i * half_tokens);
       bool ok = true;
-      int u = 0;                             // tiles K_0 V_0 K_1 V_1 ...
-      for (; u < 2 * ((n_all + 1) / 2); ++u) {
-        const int s = u % S;
-        if (u >= S && !mbar_wait(&kv_empty[s], ((u / S) - 1) & 1)) { ok = false; break; }
-        mbar_arrive_expect_tx(&kv_full[s], (uint32_t)C::kTile);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(2 * C::kHalves * half_tokens * a.group * 128));
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tma_load_3d(smem_u32(ring) + (uint32_t)(s * C::kTile + h * C::kBlock),
-                      (u & 1) ? &tv : &tk, &kv_full[s], h * 64, kvh, t.k0 + (u >> 1) * kPtKeys);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(smem_u32(smem) + (uint32_t)(i * C::kTile + h * C::kBlock), &tq, q_full,
+                        h * 64, kvh * a.group, t.q0 + t.t0 + i * half_tokens);
+        int u = 0;                           // tiles K_0 V_0 K_1 V_1 ...
+        for (; u < 2 * (last_tile + 1); ++u) {
+          const int s = u % S;
+          if (u >= S && !mbar_wait(&kv_empty[s], ((u / S) - 1) & 1)) { ok = false; break; }
+          mbar_arrive_expect_tx(&kv_full[s], (uint32_t)C::kTile);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(smem_u32(ring) + (uint32_t)(s * C::kTile + h * C::kBlock),
+                        (u & 1) ? &tv : &tk, &kv_full[s], h * 64, kvh, t.k0 + (u >> 1) * kPtKeys);
+        }
+        // a wait that gave up: the copies in flight still land before the exit
+        if (!ok)
+          for (int w = u > S ? u - S : 0; w < u; ++w) mbar_wait(&kv_full[w % S], (w / S) & 1);
       }
-      // a wait that gave up: the copies in flight still land before the exit
-      if (!ok)
-        for (int w = u > S ? u - S : 0; w < u; ++w) mbar_wait(&kv_full[w % S], (w / S) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && v_tail) {
+        // values behind the sequence (another's, or whatever lies there) are
+        // zeroed, so that a masked probability times one of them is 0
+        const int e = 2 * last_tile + 1, r0 = t.kl - last_tile * kPtKeys;
+        if (__all_sync(0xffffffffu, mbar_wait(&kv_full[e % S], (uint32_t)((e / S) & 1)))) {
+          for (int x = r0 * 8 + lane; x < kPtKeys * 8; x += 32)        // rows of 128 bytes
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              sts_v4(smem_u32(ring) + (uint32_t)((e % S) * C::kTile + h * C::kBlock + x * 16),
+                     make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_clean);
+        }
+      }
     } else if (warp == 17 && elect_one() && n_all > 0) {
       // -------------------------------------------------------- MMA issuer
       const uint64_t q_desc = sw128_desc(smem_u32(smem)), k_desc = sw128_desc(smem_u32(ring));
@@ -671,7 +696,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int sk = s + 1 == S ? 0 : s + 1;               // K of step u + 2
         const uint32_t phk = s + 1 == S ? ph ^ 1 : ph;
         const bool more = u + 2 < n_all;
-        if (!(u & 1)) ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk));
+        if (!(u & 1)) ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk)) &&
+                           (!v_tail || u >> 1 < last_tile || mbar_wait(v_clean, 0));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!ok || u >= n_steps[i]) continue;
@@ -854,7 +880,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       if (a.lse && cg == 0 && r < rows)
         a.lse[(int64_t)(t.q0 + token) * a.Hq + kvh * a.group + r % a.group] =
-            l == 0.0f ? -INFINITY : (m * c + log2f(l)) * 0.69314718055994531f;
+            l == 0.0f ? -INFINITY
+                      : ((m == -INFINITY ? 0.0f : m * c) + log2f(l)) * 0.69314718055994531f;
     }
     // rows with a result that is not finite are done again, the pair's warps
     // taking turns; both warps' stores come first

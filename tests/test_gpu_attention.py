@@ -249,6 +249,26 @@ def test_prompt_extreme_scores(D):
     run_prompt(q * 8, k, v, [0, n], [0, n])
 
 
+@pytest.mark.parametrize("scale", [1e-40, 1e-20, 3.0, 1e30])
+@pytest.mark.parametrize("n", [40, 400])
+def test_prompt_scales_from_tiny_to_huge(scale, n):
+    """With a vanishing scale every key weighs the same; with a huge one the largest score takes all (its score is 0, so
+    that products stay finite)."""
+    rng = np.random.default_rng(35)
+    q, k, v = rand(rng, n, 4, 64).abs(), -rand(rng, n, 1, 64).abs() - 0.1, rand(rng, n, 1, 64)
+    k[::7] = 0
+    if scale > 100:
+        k[1:] = torch.where(k[1:] == 0, torch.tensor(-1.0, dtype=BF), k[1:])
+    y, lse = B.bitnet_attn_prompt(q.cuda(), k.cuda(), v.cuda(), i32([0, n]), scale=scale, want_lse=True)
+    yh, lh = y.double().cpu().numpy(), lse.cpu().numpy()
+    if scale > 100:                                    # weights 1 for the first key, 0 for the others
+        assert np.array_equal(yh, np.broadcast_to(f64(v[0, 0]), yh.shape)) and np.allclose(lh, 0, atol=1e-6)
+    else:
+        for t, h, *want in A.prompt(f64(q), f64(k), f64(v), [0, n], [0, n], np.float64(np.float32(scale)),
+                                    rows={0, 1, 31, 32, 100, 255, 256, n - 1}):
+            check_row(yh[t, h], lh[t, h], want, (t, h))
+
+
 def test_prompt_growing_scores():
     """Scores that grow along the keys move the running maximum at every step."""
     rng = np.random.default_rng(5)
@@ -275,6 +295,19 @@ def test_prompt_fused_projection_strides_and_scale():
     assert bool((ybuf[:, :8] == 7).all()) and bool((ybuf[:, 8 + Hq * D:] == 7).all())
     one = B.bitnet_attn_prompt(q[:1], k[:1], v[:1], i32([0, 1]))[0]          # one token: its own value
     assert torch.equal(one[0], v[0].repeat_interleave(Hq // Hkv, 0))
+
+
+def test_prompt_overlapping_bounds_stay_inside():
+    """Bounds that go back and forth: every second sequence is refused, the others overlap; nothing is written outside."""
+    rng = np.random.default_rng(36)
+    T = 300
+    q, k, v = (rand(rng, T, h, 64).cuda() for h in (4, 1, 1))
+    out = guarded((T, 4, 64), BF)
+    want = B.bitnet_attn_prompt(q, k, v, i32([0, T]))[0]
+    B.bitnet_attn_prompt(q, k, v, i32([0, T] * 200), y=out.t)
+    assert B.bitnet_last_device_status() == 1
+    out.check()
+    assert torch.allclose(out.t, want, atol=0.02)
 
 
 def test_prompt_bad_bounds_are_recorded():
@@ -614,6 +647,35 @@ def test_pool_refusals_change_nothing():
     B.bitnet_kv_free(pool, i32([-1, 9]))
     assert B.bitnet_last_device_status() == 9
     same_tables(pool, host)
+
+
+def test_binding_refuses_other_types():
+    x = torch.zeros(4, 2, 64, device="cuda")
+    c = i32([0, 4])
+    h = x.to(BF)
+    for bad in (x.half(), x, x.to(torch.int32)):
+        for args in ((bad, h, h), (h, bad, h), (h, h, bad)):
+            with pytest.raises(ValueError):
+                B.bitnet_attn_prompt(*args, c)
+        with pytest.raises(ValueError):
+            B.bitnet_attn_prompt(h, h, h, c, y=bad)
+    with pytest.raises(ValueError):
+        B.bitnet_attn_prompt(h, h, h, c.long())
+    with pytest.raises(ValueError):
+        B.bitnet_attn_prompt(h.transpose(1, 2), h, h, c)
+    with pytest.raises(B.BitnetError):                 # 96-wide heads
+        B.bitnet_attn_prompt(*[torch.zeros(4, 2, 96, dtype=BF, device="cuda")] * 3, c)
+    with pytest.raises(B.BitnetError):                 # one row for every token
+        B.bitnet_attn_prompt(h[:1].expand(4, 2, 64), h, h, c)
+    pool = B.bitnet_kv_pool(2, 2, 4, 16)
+    pages = torch.zeros(4, 2, 16, 64, dtype=BF, device="cuda")
+    for bad in (pages.half(), pages[:3], pages[:, :, :8], torch.zeros(4, 2, 16, 128, dtype=BF, device="cuda")):
+        with pytest.raises(ValueError):
+            B.bitnet_attn_decode(h[:2], bad, bad, pool)
+        with pytest.raises(ValueError):
+            B.bitnet_kv_append(h, h, c, pool, bad, bad)
+    with pytest.raises(ValueError):
+        B.bitnet_kv_extend(pool, torch.ones(2, device="cuda"))
 
 
 def test_copy_pages_skips_pairs_outside_the_pool():
