@@ -78,7 +78,7 @@ DecodeWs decode_ws(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   const int g = (int)(Hq / Hkv);
   w.hb = (g + 15) / 16;
   w.rows = (g + w.hb - 1) / w.hb;
-  const size_t n = (size_t)2 * kDecMaxCtas * w.rows;
+  const size_t n = (size_t)2 * kDecMaxSms * (D == 64 ? dec_ctas<64>() : dec_ctas<128>()) * w.rows;
   w.part = 0;
   w.ml = al256(n * D * 4);
   w.first = w.ml + al256(n * 8);
@@ -266,7 +266,8 @@ bitnet_status bitnet_attn_decode(const uint16_t* q, int64_t q_stride, const uint
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);
   a.first_unit = reinterpret_cast<int64_t*>(ws + w.first);
-  const int ctas = 2 * d.num_sms < kDecMaxCtas ? 2 * d.num_sms : kDecMaxCtas;
+  const int ctas = (d.num_sms < kDecMaxSms ? d.num_sms : kDecMaxSms) *
+                   (D == 64 ? dec_ctas<64>() : dec_ctas<128>());
   cudaStream_t s = as_stream(stream);
   if (D == 64) return w.rows <= 8 ? decode_launch<64, 1>(a, ctas, s) : decode_launch<64, 2>(a, ctas, s);
   return w.rows <= 8 ? decode_launch<128, 1>(a, ctas, s) : decode_launch<128, 2>(a, ctas, s);

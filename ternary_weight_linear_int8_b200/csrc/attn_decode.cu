@@ -32,8 +32,17 @@ namespace bitnet {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecUnit = 16 * kDecWarps;   // tokens per unit
-constexpr int kDecStages = 3;
-constexpr int kDecMaxCtas = 320;           // workspace slots: two per CTA
+// CTAs per SM and stages of a warp's ring.  With D = 128 two CTAs of three
+// stages of 8 KB (128 KB of copies ahead of the computation per SM); three of
+// two stages are slower on long contexts (100003 tokens of 64 heads 71.9 -> 73.6
+// us).  With D = 64 the same bytes are twice the tokens, and a third CTA hides
+// more of each step's latency (64 users of 2000 tokens, 16 heads: 98.0 -> 86.3
+// us; with three stages 88.4, four CTAs 92.4).
+template <int D>
+constexpr int dec_ctas() { return D == 64 ? 3 : 2; }
+template <int D>
+constexpr int dec_stages() { return D == 64 ? 2 : 3; }
+constexpr int kDecMaxSms = 160;            // workspace slots: two per CTA
 
 struct AttnDecodeArgs {
   const uint16_t* q;        // [B, Hq, D], rows q_stride apart
@@ -93,16 +102,16 @@ template <int D>
 constexpr int dec_stage_bytes() { return 2 * 16 * D * 2; }   // 16 keys and values
 template <int D, int NT>
 constexpr int dec_smem_bytes() {
-  return kDecWarps * kDecStages * dec_stage_bytes<D>() + 2 * 8 * NT * (D + 4) * 4;
+  return kDecWarps * dec_stages<D>() * dec_stage_bytes<D>() + 2 * 8 * NT * (D + 4) * 4;
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const AttnDecodeArgs a) {
+__global__ void __launch_bounds__(kDecWarps * 32, dec_ctas<D>()) attn_decode_kernel(const AttnDecodeArgs a) {
   extern __shared__ __align__(128) uint8_t dsm[];
   __shared__ long long s_scan[kDecWarps + 1];
   __shared__ int s_start[3];
   __shared__ float s_ml[2][kDecWarps][16];
-  constexpr int kStage = dec_stage_bytes<D>();
+  constexpr int kStage = dec_stage_bytes<D>(), kDecStages = dec_stages<D>();
   constexpr int CH = D / 8;                  // 16-byte chunks per row
   constexpr int KT = D / 16;                 // 16-wide steps over D
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
