@@ -344,25 +344,24 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
 // nothing.
 //
 // Measured (device time): 4096 tokens of 20 heads of 128 on 4 key-value heads
-// 99 us (865 TFLOP/s), 16384 tokens 1.21 ms (1138, power capped), 4096 tokens of
-// 16 heads of 64 66 us.  With D = 128 the bound is shared memory: a score MMA
-// reads Q and K at the full 128 bytes a clock (8 x 6 KB per half and step),
-// the output MMAs read V at half of it, and the ring's TMA writes come on
-// top; the MMAs alone, with no softmax, take 1650 cycles a step of 1239 that
-// they take without the ring's traffic.  With D = 64 it is the exponentials
-// (16 a clock and SM).  Alternatives: scores 128 keys wide and single buffered
-// (less shared-memory traffic, but softmax and MMAs of a half in turn): 97 us,
-// 1.18 ms and 72 us; one thread per whole row (8 softmax warps): 105 us and
-// more; two issuing warps, one per half (the halves fall into step and wait
-// for the same unit): 108 us; a quarter of the exponentials as polynomials on
-// the fp32 pipe: 104 us, 1.28 ms and 70 us (the longer instruction stream
-// costs more than the special function unit saves).
+// 88 us (977 TFLOP/s), 16384 tokens 1.19 ms (1158, power capped), 4096 tokens of
+// 16 heads of 64 71 us.  A step of both halves takes about 1850 cycles with
+// D = 128.  Its MMAs back to back take 1239 (the score MMAs read Q and K from
+// shared memory at its full 128 bytes a clock, so 48 cycles instead of 32 for
+// 128 x 64 x 16); with the barriers handed over but no softmax 1560; taking the
+// ring's TMA traffic away changes nothing.  The four softmax warps of a
+// scheduler need 1024 cycles for the exponentials alone (4 a clock), which
+// is the bound with D = 64.  What the issuing thread does between MMAs counts:
+// its loop is unrolled over halves and steps, one thread issues everything.
+// Alternatives, 4096 tokens of 20 heads: scores 128 keys wide and single
+// buffered (a half's softmax and MMAs in turn) 97 us; one thread per whole row
+// (8 softmax warps) 105 us and more; two issuing warps, one per half (the
+// halves fall into step and wait for the same unit) 108 us; a quarter of the
+// exponentials as polynomials on the fp32 pipe 104 us (against 99 then); waits
+// that poll in a plain loop 101 us.
 constexpr int kPtKeys = 128, kPtSub = 64;
 constexpr int kPtThreads = 640;
 constexpr int kPtRegs = 96;                  // 65536 / 640, in steps of 8
-constexpr int kPtRegsSoftmax = 104, kPtRegsIssue = 64;
-static_assert(512 * kPtRegsSoftmax + 128 * kPtRegsIssue <= kPtThreads * kPtRegs,
-              "the warpgroups' registers come from the launch's");
 template <int D>
 struct PtCfg {
   static constexpr int kHalves = D / 64;                  // 128-byte wide column blocks
@@ -608,7 +607,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const bool v_tail = n_all > 0 && (last_tile + 1) * kPtKeys > t.kl;
 
   if (warp >= 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsIssue));
     if (warp == 16 && n_all > 0) {
       // ------------------------------------------------------ TMA producer
       bool ok = true;
@@ -654,71 +652,79 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // -------------------------------------------------------- MMA issuer
       const uint64_t q_desc = sw128_desc(smem_u32(smem)), k_desc = sw128_desc(smem_u32(ring));
       const uint64_t v_desc = sw128_mn_desc(smem_u32(ring), C::kBlock);
-      // S_i[u & 1] = Q_i K^T for step u, its 64 keys in stage s
-      auto scores = [&](int i, int u, int s) {
-        const uint32_t st = tmem + (uint32_t)(i * 128 + (u & 1) * kPtSub);
+      // S_i[b] = Q_i K^T, the 64 keys of step b of the tile at k_tile
+      auto scores = [&](int i, int b, uint64_t k_tile) {
         const uint64_t qd = q_desc + (uint64_t)(i * (C::kTile >> 4));
-        const uint64_t kd = k_desc + (uint64_t)(s * (C::kTile >> 4) + (u & 1) * (kPtSub * 128 >> 4));
+        const uint64_t kd = k_tile + (uint64_t)(b * (kPtSub * 128 >> 4));
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t o = (uint64_t)((x >> 2) * (C::kBlock >> 4) + 2 * (x & 3));
-          tc_mma_bf16(st, qd + o, kd + o, C::kIdescS, x > 0);
+          tc_mma_bf16(tmem + (uint32_t)(i * 128 + b * kPtSub), qd + o, kd + o, C::kIdescS, x > 0);
         }
-        tc_commit(&s_full[2 * i + (u & 1)]);
+        tc_commit(&s_full[2 * i + b]);
       };
-      // O_i (+)= P_i[u & 1] V for step u, its 64 values in stage s
-      auto outputs = [&](int i, int u, int s) {
-        const uint64_t vd = v_desc + (uint64_t)(s * (C::kTile >> 4) + (u & 1) * (kPtSub * 128 >> 4));
+      // O_i (+)= P_i[b] V, the 64 values of step b of the tile at v_tile
+      auto outputs = [&](int i, int b, uint64_t v_tile, bool add) {
+        const uint64_t vd = v_tile + (uint64_t)(b * (kPtSub * 128 >> 4));
         const uint32_t ot = tmem + (uint32_t)(256 + i * D);
-        const uint32_t pt = tmem + (uint32_t)(i * 128 + (u & 1) * kPtSub);
-        tc_mma_bf16_ts(ot, pt, vd, C::kIdescO, u > 0);
+        const uint32_t pt = tmem + (uint32_t)(i * 128 + b * kPtSub);
+        tc_mma_bf16_ts(ot, pt, vd, C::kIdescO, add);
 #pragma unroll
         for (int x = 1; x < kPtSub / 16; ++x)
           tc_mma_bf16_ts(ot, pt + 8 * x, vd + x * (2048 >> 4), C::kIdescO, 1);
         tc_commit(&o_done[i]);
-        if (u + 1 == n_steps[i]) tc_commit(&o_full[i]);
       };
       // scores run two steps ahead of the outputs; K of tile j and V of tile j
       // are ring entries 2 j and 2 j + 1
+      const int n0 = n_steps[0], n1 = n_steps[1];
       bool ok = mbar_wait(q_full, 0) && mbar_wait(&kv_full[0], 0);
       if (ok) {
         tc_fence_after();
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (u < n_steps[i]) scores(i, u, 0);
+            if (b < (i ? n1 : n0)) scores(i, b, k_desc);
         tc_commit(&kv_empty[0]);
       }
-      int s = 1;                             // stage and phase of the step's V
+      int s = 1;                             // stage and phase of V_j
       uint32_t ph = 0;
-      for (int u = 0; u < n_all && ok; ++u) {
-        const int sk = s + 1 == S ? 0 : s + 1;               // K of step u + 2
-        const uint32_t phk = s + 1 == S ? ph ^ 1 : ph;
-        const bool more = u + 2 < n_all;
-        if (!(u & 1)) ok = mbar_wait(&kv_full[s], ph) && (!more || mbar_wait(&kv_full[sk], phk)) &&
-                           (!v_tail || u >> 1 < last_tile || mbar_wait(v_clean, 0));
+      for (int j = 0; j <= last_tile && ok; ++j) {
+        const int sk = s + 1 == S ? 0 : s + 1;               // K_{j+1}
+        const uint32_t phk = s + 1 == S ? ph ^ 1 : ph, par = (uint32_t)(j & 1);
+        const uint64_t v_tile = v_desc + (uint64_t)(s * (C::kTile >> 4));
+        const uint64_t k_tile = k_desc + (uint64_t)(sk * (C::kTile >> 4));
+        ok = mbar_wait(&kv_full[s], ph) && (j == last_tile || mbar_wait(&kv_full[sk], phk)) &&
+             (!v_tail || j < last_tile || mbar_wait(v_clean, 0));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || u >= n_steps[i]) continue;
-          ok = mbar_wait(&p_full[2 * i + (u & 1)], (uint32_t)((u >> 1) & 1));
-          if (!ok) continue;
-          tc_fence_after();
-          outputs(i, u, s);
-          if (u + 2 < n_steps[i]) scores(i, u + 2, sk);
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int left = (i ? n1 : n0) - 2 * j - b;      // steps from this one on
+            if (!ok || left <= 0) continue;
+            ok = mbar_wait(&p_full[2 * i + b], par);
+            if (!ok) continue;
+            tc_fence_after();
+            outputs(i, b, v_tile, j + b > 0);
+            if (left > 2) scores(i, b, k_tile);
+            if (left == 1) tc_commit(&o_full[i]);
+          }
+        if (ok) {
+          tc_commit(&kv_empty[s]);
+          if (j < last_tile) tc_commit(&kv_empty[sk]);
         }
-        if (ok && ((u & 1) || u + 1 == n_all)) tc_commit(&kv_empty[s]);
-        if (ok && more && ((u & 1) || u + 3 == n_all)) tc_commit(&kv_empty[sk]);
-        if (u & 1) {
-          s = sk + 1 == S ? 0 : sk + 1;
-          ph = sk + 1 == S ? phk ^ 1 : phk;
-        }
+        s = sk + 1 == S ? 0 : sk + 1;
+        ph = sk + 1 == S ? phk ^ 1 : phk;
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoftmax));
+    // The registers the launch gave (no more are asked for).  Without the
+    // statement the compiler schedules the loop below worse: 4096 tokens of 20
+    // heads 91.8 instead of 87.9 us.  Giving the softmax warps 104 and the others
+    // 64 spills in the issuing thread: 98 us.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegs));
     const int i = warp >> 3, cg = (warp >> 2) & 1;       // row half, column half
     const int r = 32 * (warp & 3) + lane;    // this thread's row
     const int pair = 1 + 4 * i + (warp & 3);
