@@ -147,12 +147,12 @@ bitnet_status prompt_tile_launch(AttnPromptArgs a, int num_sms, cudaStream_t s) 
   a.tile_tokens = 2 * half;
   int64_t grid = prompt_ctas(a, a.tile_tokens);
   // Too few tiles for the SMs: tiles of one half each, twice as many.  A step
-  // of one half takes about 0.65 of the time of two, with D = 64 (bound by the
-  // exponentials) less.  One wave of halves: 512 / 1024 tokens of 20 heads 14.8 /
-  // 22.8 -> 11.0 / 16.6 us, 200 rows on 8000 keys 131 -> 87.  More than one wave
-  // pays with D = 64 (1000 rows on 5000 keys of 16 heads 68 -> 55 us, 2048 tokens
-  // 31 -> 28) and not with D = 128 (512 rows on 4096 keys of 64 heads 71 -> 90,
-  // 512 tokens of 64 heads 15.2 -> 19.1).
+  // of one half takes about 0.7 of the time of two, with D = 64 (bound by the
+  // exponentials) less.  One wave of halves: 512 / 1024 tokens of 20 heads 13.4 /
+  // 20.0 -> 10.6 / 16.0 us, 200 rows on 8000 keys 115 -> 83.  More than one wave
+  // pays with D = 64 (1000 rows on 5000 keys of 16 heads 69 -> 56 us, 2048 tokens
+  // 32 -> 28) and not with D = 128 (512 rows on 4096 keys of 64 heads 64 -> 86,
+  // 512 tokens of 64 heads 14.1 -> 18.4).
   if (prompt_ctas(a, half) <= num_sms || (D == 64 && grid <= num_sms)) {
     a.tile_tokens = half;
     grid = prompt_ctas(a, half);
@@ -208,12 +208,12 @@ bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint
   a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.group = (int)(Hq / Hkv);
   a.scale_log2 = (float)((double)scale * kLog2e);
   // Very short prompts, few of them: the warp kernel starts faster (no tensor
-  // memory, no tensor maps).  20 heads of 128, one prompt of 1 / 64 / 128 / 200
-  // tokens: 4.2 / 6.0 / 7.3 / 9.3 us against the tile kernel's 6.1 / 6.6 / 7.3 /
-  // 8.3; 16 heads of 64, 64 / 128 / 200 / 300 tokens: 4.2 / 5.2 / 6.3 / 7.9
-  // against 5.0 / 6.3 / 6.7 / 7.5.
+  // memory, no tensor maps).  20 heads of 128, one prompt of 1 / 64 / 96 / 200
+  // tokens: 4.3 / 6.0 / 7.4 / 9.4 us against the tile kernel's 5.8 / 6.2 / 6.7 /
+  // 7.8; 16 heads of 64, 64 / 128 / 200 / 300 tokens: 4.3 / 5.2 / 6.4 / 7.9
+  // against 5.0 / 6.4 / 6.7 / 7.6.
   const bool few = prompt_ctas(a, kPwRows / a.group) * 2 <= 3 * d.num_sms &&
-                   Tk <= (D == 64 ? 192 : 96) * B;
+                   Tk <= (D == 64 ? 192 : 64) * B;
   if (few)
     return D == 64 ? prompt_warp_launch<64>(a, as_stream(stream))
                    : prompt_warp_launch<128>(a, as_stream(stream));

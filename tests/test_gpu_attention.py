@@ -226,9 +226,10 @@ def test_prompt_poison_behind_the_causal_border(D, bad, where):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("where,bad", [("v", NAN), ("v", -INF), ("k", NAN), ("q", INF)])
-def test_short_prompt_poison(D, where, bad):
+@pytest.mark.parametrize("n", [60, 70])
+def test_short_prompt_poison(n, D, where, bad):
     rng = np.random.default_rng(34)
-    Hq, Hkv, n = 4, 2, 70
+    Hq, Hkv = 4, 2
     q, k, v = rand(rng, n, Hq, D).abs(), rand(rng, n, Hkv, D), rand(rng, n, Hkv, D)
     dict(q=q, k=k, v=v)[where][45, 1, 5] = bad
     run_prompt(q, k, v, [0, n], [0, n], lse=where == "v")
