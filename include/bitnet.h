@@ -539,9 +539,9 @@ BITNET_API size_t bitnet_kv_workspace_size(int64_t n_slots, int64_t n_pages);
  * A slot may be named once.  All or nothing: with bad arguments or too few
  * free pages nothing changes.
  * short_pages  one int32 on the device or NULL: 0 when done, the number of
- *          pages that were lacking (at least so many, where one slot alone
- *          wants more than the pool has), or -1 for bad arguments (an unknown
- *          or repeated slot, add < 0, more than max_pages * page_size tokens).
+ *          pages that were lacking (at most INT32_MAX), or -1 for bad
+ *          arguments (an unknown or repeated slot, add < 0, more than
+ *          max_pages * page_size tokens).
  */
 BITNET_API bitnet_status bitnet_kv_extend(const bitnet_kv_tables* kv, const int32_t* slots,
                                           const int32_t* add, int64_t n, int32_t* short_pages,

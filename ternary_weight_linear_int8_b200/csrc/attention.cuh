@@ -104,4 +104,19 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int* red, int& total) 
   return inc - v + (warp ? red[warp - 1] : 0);
 }
 
+// Sum over the block's threads (at most 1024), for all of them.  `red` holds
+// 32 values.
+__device__ __forceinline__ long long block_sum(long long v, long long* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();                 // the previous call's values are read
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < nw ? red[lane] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 }  // namespace bitnet

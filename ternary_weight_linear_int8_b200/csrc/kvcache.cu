@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
                                                                int32_t* ws) {
   __shared__ uint32_t used[kKvMaxSlots / 32];
   __shared__ int red[33];
+  __shared__ long long red64[32];
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -133,15 +134,16 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
     }
     return;
   }
-  // a thread's wish is held at the number of pages, so the sum cannot overflow
-  int total;
-  block_exclusive_sum((int)min(want, (long long)min(kv.n_pages, 0x7fffffff / kKvThreads)), red,
-                      total);
-  const int got = list_free_pages(kv.refs, kv.n_pages, total, ws, red);
-  if (got < total) {
+  // The sum is 64 bits wide: a row may want more than the pool has, and all
+  // rows together more than 2^31.  No more pages than there are get listed, and
+  // the call goes on only if the list holds every page that it will take.
+  const long long wanted = block_sum(want, red64);
+  const int got = list_free_pages(kv.refs, kv.n_pages, (int)min(wanted, (long long)kv.n_pages), ws,
+                                  red);
+  if (got < wanted) {
     if (threadIdx.x == 0) {
       record_error(BITNET_ERR_PAGES);
-      if (short_pages) *short_pages = total - got;
+      if (short_pages) *short_pages = (int)min(wanted - got, 0x7fffffffll);
     }
     return;
   }
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
       r.e0 = (old + kv.page_size - 1) / kv.page_size;
       r.e1 = (len + kv.page_size - 1) / kv.page_size;
     }
-    if (total > 0) {
+    if (got > 0) {
       const int k = count_missing(kv, r);
       int sum;
       int at = taken + block_exclusive_sum(k, red, sum);

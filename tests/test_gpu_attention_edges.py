@@ -1,0 +1,75 @@
+"""GPU tests of the attention and cache operators at the ends of their documented ranges: demands above the pool, damaged
+tables and bounds, scores and values at the ends of fp32's range.  Definitions and bounds as in test_gpu_attention.py."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A
+from ternary_weight_linear_int8_b200 import bitnet as B
+from tests import test_gpu_attention as T
+
+pytestmark = pytest.mark.gpu
+
+
+
+@pytest.fixture(autouse=True)
+def _status_clean():
+    yield
+    assert B.bitnet_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ cache
+@pytest.mark.parametrize("add,slots", [([150 * 16], [0]), ([101 * 16], [1]), ([60 * 16, 60 * 16], [0, 1]),
+                                       ([1, 200 * 16 - 1, 0], [2, 0, 1])])
+def test_extend_wants_more_than_an_empty_pool_has(add, slots):
+    host = A.Pool(3, 200, 100, 16)
+    pool, short = T.to_device(host), T.i32([77])
+    want = host.extend(add, slots)
+    assert want > 0
+    B.bitnet_kv_extend(pool, T.i32(add), slots=T.i32(slots), short_pages=short)
+    assert B.bitnet_last_device_status() == 9
+    assert int(short) == want
+    T.same_tables(pool, host)
+    # exactly all of it is granted afterwards
+    assert host.extend([100 * 16], [slots[0]]) == 0
+    B.bitnet_kv_extend(pool, T.i32([100 * 16]), slots=T.i32(slots[:1]), short_pages=short)
+    assert int(short) == 0
+    T.same_tables(pool, host)
+
+
+def test_extend_more_rows_than_threads():
+    host = A.Pool(2300, 3, 4000, 16)
+    rng = np.random.default_rng(41)
+    pool, short = T.to_device(host), T.i32([77])
+    for add in (rng.integers(0, 40, 2300), np.full(2300, 30), np.full(2300, 8)):
+        add = np.minimum(add, 48 - host.lens).tolist()
+        want = host.extend(add)
+        B.bitnet_kv_extend(pool, T.i32(add), short_pages=short)
+        assert int(short) == want and B.bitnet_last_device_status() == (9 if want else 0)
+        T.same_tables(pool, host)
+
+
+def test_extend_by_more_pages_than_two_million():
+    """One slot that takes 2.5 million pages of a pool of three; the tables alone, no pages behind them."""
+    n_pages, entries = 3_000_000, 2_500_000
+    pool, short = B.bitnet_kv_pool(2, entries, n_pages, 16), T.i32([77])
+    pool.refs[100_000:] = 1                                    # too few are free
+    B.bitnet_kv_extend(pool, T.i32([entries * 16]), short_pages=short)
+    assert B.bitnet_last_device_status() == 9 and int(short) == entries - 100_000
+    assert bool((pool.table == -1).all()) and bool((pool.lens == 0).all()) and int(pool.refs.sum()) == 2_900_000
+    pool.refs[100_000:] = 0
+    pool.refs[5:10] = 3
+    B.bitnet_kv_extend(pool, T.i32([entries * 16 - 3]), short_pages=short)
+    assert int(short) == 0 and pool.lens.tolist() == [entries * 16 - 3, 0]
+    pages = torch.cat([torch.arange(5), torch.arange(10, entries + 5)]).to(torch.int32)
+    assert torch.equal(pool.table[0].cpu(), pages) and bool((pool.table[1] == -1).all())
+    refs = torch.zeros(n_pages, dtype=torch.int32)
+    refs[:entries + 5] = 1
+    refs[5:10] = 3
+    assert torch.equal(pool.refs.cpu(), refs)
+    # both rows at once want more than 2^21 pages that are not there
+    B.bitnet_kv_extend(pool, T.i32([3, entries * 16]), short_pages=short)
+    assert B.bitnet_last_device_status() == 9 and int(short) == entries - (n_pages - entries - 5)
+    assert pool.lens.tolist() == [entries * 16 - 3, 0] and torch.equal(pool.refs.cpu(), refs)
