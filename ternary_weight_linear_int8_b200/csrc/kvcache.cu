@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a) {
   int row = 0;
   if (slot_ok(a.kv, s)) {
     const int len = slot_len(a.kv, s);
-    const int64_t pos = (int64_t)len - (c1 - c0) + (r - c0);
+    // below len, since r < c1; in 64 bits, whatever the bounds are
+    const int64_t pos = (int64_t)len - c1 + r;
     if (len >= 0 && pos >= 0) {
       const int e = (int)(pos / a.kv.page_size);
       row = (int)(pos - (int64_t)e * a.kv.page_size);

@@ -13,7 +13,6 @@ from tests import test_gpu_attention as T
 pytestmark = pytest.mark.gpu
 
 
-
 @pytest.fixture(autouse=True)
 def _status_clean():
     yield
@@ -73,3 +72,27 @@ def test_extend_by_more_pages_than_two_million():
     B.bitnet_kv_extend(pool, T.i32([3, entries * 16]), short_pages=short)
     assert B.bitnet_last_device_status() == 9 and int(short) == entries - (n_pages - entries - 5)
     assert pool.lens.tolist() == [entries * 16 - 3, 0] and torch.equal(pool.refs.cpu(), refs)
+
+
+@pytest.mark.parametrize("c", [[-2_000_000_000, 2_000_000_000], [-2 ** 31, 2 ** 31 - 1], [-2 ** 31, 25, 25],
+                               [0, 2 ** 31 - 1], [-1_500_000_000, 700_000_000, 2 ** 31 - 1]])
+def test_append_bounds_from_end_to_end_of_int32(c):
+    """Bounds whose difference does not fit 32 bits: no row has a position, or only those that the length holds."""
+    rng = np.random.default_rng(42)
+    pool, host, kp, vp, _, _ = T.make_cache(rng, [20, 20], 16, 2, 64, poison=0.0)
+    want = [kp.cpu().clone(), vp.cpu().clone()]
+    k = T.rand(rng, 30, 2, 64)
+    skipped = False
+    for r in range(30):
+        b = max(i for i in range(len(c)) if c[i] <= r)
+        if b == len(c) - 1:
+            continue
+        pos = 20 - c[b + 1] + r
+        skipped |= pos < 0
+        if pos >= 0:
+            for w in want:
+                w[host.table[b, pos // 16], :, pos % 16] = k[r]
+    B.bitnet_kv_append(k.cuda(), k.cuda(), T.i32(c), pool, kp, vp)
+    assert B.bitnet_last_device_status() == (9 if skipped else 0)
+    assert torch.equal(kp.cpu(), want[0]) and torch.equal(vp.cpu(), want[1])
+    T.same_tables(pool, host)
