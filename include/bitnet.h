@@ -594,7 +594,8 @@ BITNET_API bitnet_status bitnet_attn_decode(const uint16_t* q, int64_t q_stride,
  *          bitnet_kv_copy_pages).
  * short_pages  as bitnet_kv_extend.  All or nothing.  Bad arguments are a slot
  * outside the tables, a child that holds tokens, is named twice or is also a
- * parent.  A parent may be named many times.
+ * parent, and a parent whose tokens lie on an entry without a page of the pool.
+ * A parent may be named many times.
  */
 BITNET_API bitnet_status bitnet_kv_fork(const bitnet_kv_tables* kv, const int32_t* parents,
                                         const int32_t* children, int64_t n, int32_t* pairs,

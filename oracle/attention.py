@@ -94,6 +94,9 @@ class Pool:
             return -1, []
         if len(set(children)) < len(children) or set(children) & set(parents) or any(self.lens[c] for c in children):
             return -1, []
+        held = [self.table[p, :self._pages(self.lens[p])] for p in parents]
+        if any(((t < 0) | (t >= len(self.refs))).any() for t in held):
+            return -1, []
         need = [p for p in parents if self.lens[p] % self.page_size]
         free = self._free()
         if len(free) < len(need):

@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_extend_kernel(KvTables kv, cons
 // Tables of up to this many entries are finished by the planning block itself
 // instead of a second launch: 48 forks of rows of 23 entries take 5.9 us of
 // device time in one launch and 6.4 in two (and 2 us less of the host's), 128
-// of rows of 64 entries 10.0 and 7.5; compactions of 2208 entries 4.6 and 5.2.
+// of rows of 64 entries 10.0 and 7.5 (the check of the parents' entries came to
+// both later); compactions of 2208 entries 4.6 and 5.2.
 constexpr int64_t kKvOneBlock = 4096;
 
 // Entries first, first + step, .. of the children's table rows, and the counts
@@ -207,14 +208,9 @@ __device__ __forceinline__ void fork_rows(const KvTables& kv, const int32_t* par
     const int i = (int)(x / kv.max_pages), e = (int)(x % kv.max_pages);
     const int p = parents[i], c = children[i], len = kv.lens[p], full = len / kv.page_size;
     int page = -1;
-    if (e < full) {
+    if (e < full) {                          // inside the pool: the plan has checked
       page = kv.table[(int64_t)p * kv.max_pages + e];
-      if (page < 0 || page >= kv.n_pages) {
-        record_error(BITNET_ERR_PAGES);
-        page = -1;
-      } else {
-        atomicAdd(&kv.refs[page], 1);        // integer: the order does not matter
-      }
+      atomicAdd(&kv.refs[page], 1);          // integer: the order does not matter
     } else if (e == full) {
       page = fresh[i];
     }
@@ -228,11 +224,11 @@ __device__ __forceinline__ void fork_rows(const KvTables& kv, const int32_t* par
 __global__ void __launch_bounds__(kKvThreads) kv_fork_plan_kernel(
     KvTables kv, const int32_t* parents, const int32_t* children, int n, int32_t* pairs,
     int32_t* n_pairs, int32_t* short_pages, int32_t* ws, bool one_block) {
-  __shared__ uint32_t is_child[kKvMaxSlots / 32];
+  __shared__ uint32_t is_child[kKvMaxSlots / 32], is_parent[kKvMaxSlots / 32];
   __shared__ int red[33];
   pdl_wait();
   const int words = (kv.n_slots + 31) / 32;
-  for (int i = threadIdx.x; i < words; i += kKvThreads) is_child[i] = 0;
+  for (int i = threadIdx.x; i < words; i += kKvThreads) is_child[i] = is_parent[i] = 0;
   __syncthreads();
   int32_t* fresh = ws + 4;
   int32_t* list = fresh + n;
@@ -246,16 +242,36 @@ __global__ void __launch_bounds__(kKvThreads) kv_fork_plan_kernel(
     }
     const int len = slot_len(kv, p);
     if (len < 0) { bad = true; continue; }
-    if (len % kv.page_size) {
-      const int src = kv.table[(int64_t)p * kv.max_pages + len / kv.page_size];
-      if (src < 0 || src >= kv.n_pages) bad = true;
-      ++want;
-    }
+    want += len % kv.page_size != 0;
   }
   __syncthreads();                           // every child is marked
   for (int i = threadIdx.x; i < n && !bad; i += kKvThreads)
     if ((is_child[parents[i] >> 5] >> (parents[i] & 31)) & 1u) bad = true;   // parent and child
   bad = __syncthreads_or(bad);
+  if (!bad) {
+    // every entry that a parent's tokens lie in names a page: a warp per
+    // parent, however often it is named, 16 entries a lane on their way.  Costs
+    // 0.6 us for 48 children of 6 parents of 22 entries (5.6 -> 6.2 us), 1.2 for 16
+    // children of 4 parents of 1875 (5.4 -> 6.6); loads one after the other cost 6.5
+    // there.
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < n; i += kKvThreads / 32) {
+      const int p = parents[i];
+      int again = 0;
+      if (lane == 0) again = set_bit(is_parent, p);
+      if (__shfl_sync(0xffffffffu, again, 0)) continue;
+      const int held = (kv.lens[p] + kv.page_size - 1) / kv.page_size;
+      const int32_t* t = kv.table + (int64_t)p * kv.max_pages;
+      for (int e0 = lane; e0 < held; e0 += 32 * 16) {
+        unsigned page[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) page[x] = e0 + 32 * x < held ? t[e0 + 32 * x] : 0;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) bad |= page[x] >= (unsigned)kv.n_pages;
+      }
+    }
+    bad = __syncthreads_or(bad);
+  }
   int total = 0, got = 0;
   if (!bad) {
     block_exclusive_sum(want, red, total);

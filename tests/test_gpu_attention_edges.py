@@ -96,3 +96,44 @@ def test_append_bounds_from_end_to_end_of_int32(c):
     assert B.bitnet_last_device_status() == (9 if skipped else 0)
     assert torch.equal(kp.cpu(), want[0]) and torch.equal(vp.cpu(), want[1])
     T.same_tables(pool, host)
+
+
+@pytest.mark.parametrize("max_pages", [8, 3000])                # planned and written by one launch, and by two
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, "n_pages", 2 ** 31 - 1])
+@pytest.mark.parametrize("entry", [0, 1, 3])
+def test_fork_of_a_parent_on_a_page_outside_the_pool(max_pages, bad, entry):
+    """Entry 3 is the partly filled one.  Nothing changes, in the tables of the sound parent's child neither."""
+    rng = np.random.default_rng(43)
+    pool, host, _, _, _, _ = T.make_cache(rng, [50, 20, 0, 0], 16, 1, 64, spare=6, max_pages=max_pages)
+    host.table[0, entry] = len(host.refs) if bad == "n_pages" else bad
+    pool.table.copy_(torch.from_numpy(host.table))
+    short = T.i32([77])
+    assert host.fork([1, 0], [2, 3]) == (-1, [])
+    _, n = B.bitnet_kv_fork(pool, T.i32([1, 0]), T.i32([2, 3]), short_pages=short)
+    assert B.bitnet_last_device_status() == 9
+    assert int(short) == -1 and int(n) == 0
+    T.same_tables(pool, host)
+    want, pairs = host.fork([1], [2])
+    got, n = B.bitnet_kv_fork(pool, T.i32([1]), T.i32([2]), short_pages=short)
+    assert want == 0 and int(short) == 0 and got[:int(n)].tolist() == [list(p) for p in pairs]
+    T.same_tables(pool, host)
+
+
+def test_fork_of_long_parents():
+    """Parents of more entries than a warp reads at a time; a bad one at the end of the last of 40 is found."""
+    rng = np.random.default_rng(44)
+    lens = [int(x) for x in rng.integers(1000, 3000, 40)] + [0] * 50
+    pool, host, _, _, _, _ = T.make_cache(rng, lens, 16, 1, 64, spare=60, max_pages=200)
+    keep, short = host.table[39].copy(), T.i32([77])
+    par, kids = list(range(40)) + [3, 3, 39], list(range(40, 83))
+    host.table[39, (lens[39] - 1) // 16] = -1
+    pool.table.copy_(torch.from_numpy(host.table))
+    B.bitnet_kv_fork(pool, T.i32(par), T.i32(kids), short_pages=short)
+    assert B.bitnet_last_device_status() == 9 and int(short) == -1
+    T.same_tables(pool, host)
+    host.table[39] = keep
+    pool.table.copy_(torch.from_numpy(host.table))
+    want, pairs = host.fork(par, kids)
+    got, n = B.bitnet_kv_fork(pool, T.i32(par), T.i32(kids), short_pages=short)
+    assert want == 0 and int(short) == 0 and got[:int(n)].tolist() == [list(p) for p in pairs]
+    T.same_tables(pool, host)
