@@ -589,6 +589,8 @@ _current_device = torch._C._cuda_getDevice
 
 def _run(name, dev, *args):
     """Call the entry point `name` on device ordinal `dev` and its current stream."""
+    if dev < 0:
+        raise ValueError(f"{name}: all tensors must be on a CUDA device")
     fn = getattr(_lib or lib(), name)
     if _current_device() == dev:
         st = fn(*args, _raw_stream(dev))
@@ -677,6 +679,9 @@ class KvPool:
     allocation.  Built empty by bitnet_kv_pool."""
 
     def __init__(self, buf, n_slots, max_pages, n_pages, page_size, ws=None):
+        if buf.get_device() < 0 or buf.dtype != torch.int32 or buf.dim() != 1 or not buf.is_contiguous() or \
+                buf.numel() != n_slots * max_pages + n_slots + n_pages:
+            raise ValueError("buf must be a contiguous int32 CUDA vector that holds table, lens and refs")
         self.buf, self.page_size, self.ws = buf, page_size, ws
         self.n_slots, self.max_pages, self.n_pages = n_slots, max_pages, n_pages
         self.dev = buf.get_device()

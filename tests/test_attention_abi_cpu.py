@@ -140,6 +140,25 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         B.bitnet_kv_copy_pages([], [], c, c)
 
 
+def test_binding_refuses_host_pages_and_pools_of_host_buffers(monkeypatch):
+    """Tensors that are all on the host agree with each other about their device; no pointer of theirs may reach the
+    library."""
+    def called(*a):
+        raise AssertionError("the library was called")
+
+    class Fake:
+        def __getattr__(self, name):
+            return called
+
+    monkeypatch.setattr(B, "_lib", Fake())
+    pages = [torch.zeros(6, 2, 16, 64, dtype=torch.bfloat16) for _ in range(2)]
+    pairs, n = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        B.bitnet_kv_copy_pages(pages[:1], pages[1:], pairs, n)
+    with pytest.raises(ValueError):
+        B.KvPool(torch.zeros(4 * 8 + 4 + 32, dtype=torch.int32), 4, 8, 32, 16)
+
+
 def test_oracle_row_against_direct_sums():
     rng = np.random.default_rng(0)
     q, k, v = rng.standard_normal(8), rng.standard_normal((5, 8)), rng.standard_normal((5, 8))
