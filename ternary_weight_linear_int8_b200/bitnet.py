@@ -583,8 +583,11 @@ def bitnet_ffn_tp_finish(acc, I, gamma_down, amax2, sumsq_x, sumsq_h, eps=1e-5, 
 # kept short: device ordinals instead of device objects, the raw stream handle
 # instead of a stream object.
 _BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (Both are private names that only CUDA builds of torch have: the public calls
+# stand in for them, so that importing this file needs neither.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(name, dev, *args):

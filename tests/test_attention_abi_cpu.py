@@ -4,6 +4,9 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -157,6 +160,20 @@ def test_binding_refuses_host_pages_and_pools_of_host_buffers(monkeypatch):
         B.bitnet_kv_copy_pages(pages[:1], pages[1:], pairs, n)
     with pytest.raises(ValueError):
         B.KvPool(torch.zeros(4 * 8 + 4 + 32, dtype=torch.int32), 4, 8, 32, 16)
+
+
+def test_binding_imports_without_the_private_names_of_torch():
+    """A torch built without CUDA lacks them; the refusals above need none of them."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from ternary_weight_linear_int8_b200 import bitnet as B\n"
+            "q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)\n"
+            "try: B.bitnet_attn_prompt(q, q, q, torch.zeros(2, dtype=torch.int32))\n"
+            "except ValueError: print('refused')\n")
+    got = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                         capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and got.stdout.strip() == "refused", got.stderr[-2000:]
 
 
 def test_oracle_row_against_direct_sums():
