@@ -83,53 +83,127 @@ __device__ __forceinline__ PromptTile prompt_find_tile(const AttnPromptArgs& a, 
   return t;
 }
 
-// One row by one warp in fp32 with the masked keys skipped: 32 keys at a time,
-// one per lane for the scores, then one output column set per lane.  For rows
-// whose tiled result is not finite: there a masked probability (0) times a
-// value of the same sequence that is infinite or NaN gives NaN, and this gives
-// the row's own value.
+// q . k of one row of D values each (16-byte aligned), in fp32.
+template <int D>
+__device__ __forceinline__ float row_dot(const uint16_t* q, const uint16_t* k) {
+  float dot = 0.f;
+#pragma unroll 8
+  for (int d = 0; d < D; d += 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(q + d), y = *reinterpret_cast<const uint4*>(k + d);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dot += __uint_as_float(xs[i] << 16) * __uint_as_float(ys[i] << 16);
+      dot += __uint_as_float(xs[i] & 0xffff0000u) * __uint_as_float(ys[i] & 0xffff0000u);
+    }
+  }
+  return dot;
+}
+
+// Mends one row of y, by one warp, where the tiled result is not finite though
+// the row's sum is a number.  There are three ways to that besides values that
+// the row sees.  A masked probability (0) times an infinite or NaN value of the
+// same sequence gives NaN: such a value is then among the masked keys that the
+// tile multiplied, [seen, n_end), and no NaN among the seen ones.  The sum of p v before the division can pass
+// fp32's range with values near its end: the column is then infinite without an
+// infinity of that sign among the seen values.  These columns are computed
+// again, in fp32 with the masked keys skipped and weights that are divided
+// first; all others stay.  And a row whose scores are all -inf (no_weight) is 0
+// whatever the values are.
+// Lane i has columns i D / 32 onwards.  4096 tokens of 20 heads (88 us): a NaN or
+// an infinity in a value that nearly all rows see 0.4 ms, all values NaN 0.6; an
+// infinity at position 2000 16 ms, a NaN there 10 and at position 4000 32 (the
+// rows just before it, few and long), a column of infinities 38.  Every such row
+// computed as a whole took 77 .. 92 ms, and so did rows that are NaN by a score,
+// which take no time now.
 template <int D>
 __device__ __noinline__ void prompt_row_by_warp(const AttnPromptArgs& a, const PromptTile& t,
-                                                int token, int head) {
+                                                int token, int head, int n_end, bool no_weight) {
+  constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
   const int kvh = head / a.group;
   const uint16_t* q = a.q + (int64_t)(t.q0 + token) * a.q_stride + (int64_t)head * D;
   const uint16_t* k = a.k + (int64_t)t.k0 * a.k_stride + (int64_t)kvh * D;
-  const uint16_t* v = a.v + (int64_t)t.k0 * a.v_stride + (int64_t)kvh * D;
-  const int n = token + t.kl - t.ql + 1;
-  float m = -INFINITY, l = 0.f, o[D / 32];
+  const uint16_t* v = a.v + (int64_t)t.k0 * a.v_stride + (int64_t)kvh * D + lane * V;
+  uint16_t* yr = a.y + (int64_t)(t.q0 + token) * a.y_stride + (int64_t)head * D + lane * V;
+  const int seen = max(0, token + t.kl - t.ql + 1);
+  auto columns = [](const uint16_t* p, uint32_t (&x)[V]) {   // this lane's of one row
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    if (j < n) {
-      const uint16_t* kr = k + (int64_t)j * a.k_stride;
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) dot += bf16_bits_to_float(q[d]) * bf16_bits_to_float(kr[d]);
-      s = dot * a.scale_log2;
+    for (int i = 0; i < V; i += 2) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(p)[i / 2];
+      x[i] = w & 0xffffu;
+      x[i + 1] = w >> 16;
     }
+  };
+  if (no_weight) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) *reinterpret_cast<uint32_t*>(yr + i) = 0u;
+    return;
+  }
+  uint32_t y[V], nans = 0, infs = 0, need = 0, found = 0;   // a bit per column
+  columns(yr, y);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    nans |= (uint32_t)((y[i] & 0x7fffu) > 0x7f80u) << i;
+    infs |= (uint32_t)((y[i] & 0x7fffu) == 0x7f80u) << i;
+  }
+  if (__any_sync(0xffffffffu, nans != 0)) {
+#pragma unroll 8
+    for (int j = seen; j < n_end; ++j) {
+      uint32_t x[V];
+      columns(v + (int64_t)j * a.v_stride, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) need |= (uint32_t)((x[i] & 0x7f80u) == 0x7f80u) << i;
+    }
+    need &= nans;
+  }
+  need |= infs;
+  // what the row sees may explain the column: an infinity of that sign, a NaN
+  for (int j0 = 0; j0 < seen && __any_sync(0xffffffffu, (need & ~found) != 0); j0 += 32) {
+#pragma unroll 8
+    for (int j = j0; j < min(j0 + 32, seen); ++j) {
+      uint32_t x[V];
+      columns(v + (int64_t)j * a.v_stride, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        found |= (uint32_t)(infs >> i & 1u ? x[i] == y[i] : (x[i] & 0x7fffu) > 0x7f80u) << i;
+    }
+  }
+  need &= ~found;
+  if (!__any_sync(0xffffffffu, need != 0)) return;
+  float m = -INFINITY, l = 0.f, o[V];
+  for (int j0 = 0; j0 < seen; j0 += 32) {
+    const float s = j0 + lane < seen ? row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) * a.scale_log2
+                                     : -INFINITY;
     const float top = fmaxf(m, warp_max(s));
-    const float f = m == top ? 1.f : ex2(m - top);
-    const float p = ex2(s - (top == -INFINITY ? 0.f : top));
+    l = l * (m == top ? 1.f : ex2(m - top)) + ex2(s - (top == -INFINITY ? 0.f : top));
     m = top;
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] *= f;
-    for (int x = 0; x < 32 && j0 + x < n; ++x) {
-      const float px = __shfl_sync(0xffffffffu, p, x);
-      const uint16_t* vr = v + (int64_t)(j0 + x) * a.v_stride + lane * (D / 32);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] += px * bf16_bits_to_float(vr[i]);
-    }
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* yr = a.y + (int64_t)(t.q0 + token) * a.y_stride + (int64_t)head * D + lane * (D / 32);
+  const float inv = 1.f / l;
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2)
-    *reinterpret_cast<uint32_t*>(yr + i) = pack_bf16(o[i] * inv, o[i + 1] * inv);
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int j0 = 0; j0 < seen; j0 += 32) {
+    float p = 0.f;
+    if (j0 + lane < seen)
+      p = ex2(row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) * a.scale_log2 - m) * inv;
+    for (int x0 = 0; x0 < 32; x0 += 8) {     // eight rows of values on their way
+      uint32_t w[8][V] = {};
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (j0 + x0 + x < seen) columns(v + (int64_t)(j0 + x0 + x) * a.v_stride, w[x]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float px = __shfl_sync(0xffffffffu, p, x0 + x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] += px * __uint_as_float(w[x][i] << 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (need >> i & 1u) yr[i] = (uint16_t)pack_bf16(o[i], 0.f);
 }
 
 constexpr int kPwRows = 64, kPwKeys = 64;    // rows and keys per tile
@@ -276,7 +350,7 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
     __syncthreads();                         // the buffers may be refilled
   }
   cp_async_wait<0>();
-  unsigned redo = 0;
+  unsigned redo = 0, none = 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
@@ -299,17 +373,20 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
                                          ? -INFINITY
                                          : (m[half] + log2f(l[half])) * 0.69314718055994531f;
     }
-    unsigned nan = __ballot_sync(0xffffffffu, odd != odd);
+    // a sum that is NaN makes the whole row NaN, which it is already
+    unsigned nan = __ballot_sync(0xffffffffu, odd != odd && l[half] == l[half]);
     nan |= nan >> 1;
     nan |= nan >> 2;
     redo = (nan & 0x11111111u) << half | redo;   // bit 4 i + half: row i + 8 half of the warp
+    none |= (__ballot_sync(0xffffffffu, l[half] == 0.f) & 0x11111111u) << half;
   }
   while (redo) {
     const int bit = __ffs(redo) - 1;
     redo &= redo - 1;
     const int r = warp * 16 + (bit >> 2) + 8 * (bit & 3);
     __syncwarp();
-    prompt_row_by_warp<D>(a, t, t.t0 + r / a.group, kvh * a.group + r % a.group);
+    prompt_row_by_warp<D>(a, t, t.t0 + r / a.group, kvh * a.group + r % a.group, n_keys,
+                          none >> bit & 1u);
   }
 }
 
@@ -745,7 +822,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint64_t l2[2] = {0, 0};                 // partial sums, two lanes each
     // a wait that gave up does not end the loop: both warps of a pair go on to
     // the same barriers (without further waits) and nothing is written
-    bool ok = true, poison = false;
+    bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int buf = 2 * i + (j & 1);
       const uint32_t sub = (uint32_t)((j & 1) * kPtSub);
@@ -812,7 +889,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           }
           continue;
         }
-        poison |= !(top < INFINITY);
         tmem_st16_async(pt + sub, p);
         l2[0] = f2_add(l2[0], t2[0]);
         l2[1] = f2_add(l2[1], t2[1]);
@@ -889,18 +965,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             l == 0.0f ? -INFINITY
                       : ((m == -INFINITY ? 0.0f : m * c) + log2f(l)) * 0.69314718055994531f;
     }
-    // rows with a result that is not finite are done again, the pair's warps
-    // taking turns; both warps' stores come first
-    const bool again = pair_any(pair, ok && r < rows && (poison || odd != odd));
-    if (again) {
-      *mine = ok && r < rows && (poison || odd != odd) ? 1.0f : 0.0f;
+    // rows with a result that is not finite and a sum that is a number are looked
+    // at again, the pair's warps taking turns; both warps' stores come first.  (A
+    // sum that is NaN makes the whole row NaN, which it is already.)
+    const bool mend = ok && r < rows && l == l && odd != odd;
+    if (pair_any(pair, mend)) {
+      *mine = mend ? 1.0f : 0.0f;
       pair_sync(pair);
       unsigned redo = __ballot_sync(0xffffffffu, *mine + *other > 0.0f);
+      const unsigned none = __ballot_sync(0xffffffffu, l == 0.0f);
       for (int k = 0; redo; ++k) {
-        const int row = r0 + __ffs(redo) - 1;
+        const int bit = __ffs(redo) - 1, row = r0 + bit;
         redo &= redo - 1;
         if ((k & 1) == cg)
-          prompt_row_by_warp<D>(a, t, first + row / a.group, kvh * a.group + row % a.group);
+          prompt_row_by_warp<D>(a, t, first + row / a.group, kvh * a.group + row % a.group,
+                                min(n * kPtSub, t.kl), none >> bit & 1u);
       }
     }
   }

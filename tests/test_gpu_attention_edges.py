@@ -12,6 +12,8 @@ from tests import test_gpu_attention as T
 
 pytestmark = pytest.mark.gpu
 
+NAN, INF = float("nan"), float("inf")
+
 
 @pytest.fixture(autouse=True)
 def _status_clean():
@@ -137,3 +139,56 @@ def test_fork_of_long_parents():
     got, n = B.bitnet_kv_fork(pool, T.i32(par), T.i32(kids), short_pages=short)
     assert want == 0 and int(short) == 0 and got[:int(n)].tolist() == [list(p) for p in pairs]
     T.same_tables(pool, host)
+
+
+# ------------------------------------------------ values that are not finite
+def poisoned(rng, n, Hkv, D, places):
+    """Values with the given (position, head, column or None for all, value) written over them."""
+    v = T.rand(rng, n, Hkv, D)
+    for at, h, d, x in places:
+        v[at, h, slice(None) if d is None else d] = x
+    return v
+
+
+# by column: what a row sees first, what lies behind its border, one or both infinities, all of a column, all of a row
+POISON = [
+    [(3, 0, 5, NAN), (200, 0, 7, NAN), (201, 0, 5, INF)],
+    [(3, 0, None, NAN)],
+    [(3, 0, 5, INF), (3, 0, 9, -INF), (230, 0, 5, -INF), (231, 0, 9, NAN)],
+    [(slice(None), 0, 11, INF), (slice(None), 1, None, NAN)],
+    [(slice(None), 1, 2, -INF), (100, 1, 2, NAN), (250, 0, None, INF), (251, 0, None, -INF)],
+    [(slice(40, None, 3), 0, 60, NAN), (slice(41, None, 3), 1, 1, INF)],
+]
+
+
+@pytest.mark.parametrize("places", POISON)
+@pytest.mark.parametrize("n,D", [(60, 64), (60, 128), (300, 64), (300, 128), (520, 128)])
+def test_prompt_values_that_are_not_finite(n, D, places):
+    rng = np.random.default_rng(60)
+    keep = [p for p in places if isinstance(p[0], slice) or p[0] < n]
+    v = poisoned(rng, n, 2, D, keep)
+    q, k = T.rand(rng, n, 4, D), T.rand(rng, n, 2, D)
+    rows = {0, 1, 2, 3, 4, 39, 40, 41, 42, 59, 99, 100, 101, 127, 128, 129, 185, 199, 200, 201, 202, 229, 230, 231, 232, 249,
+            250, 251, 252, 299, 400, 519}
+    T.run_prompt(q, k, v, [0, n], [0, n], rows=rows)
+
+
+@pytest.mark.parametrize("n,D", [(50, 64), (50, 128), (400, 64), (400, 128)])
+def test_prompt_values_at_the_end_of_the_range(n, D):
+    """Equal values of 2^127 and of half of it: their weighted sum before the division is past fp32's range."""
+    rng = np.random.default_rng(61)
+    q, k = T.rand(rng, n, 4, D, scale=0.1), T.rand(rng, n, 2, D)
+    v = T.rand(rng, n, 2, D)
+    v[:, 0, 3], v[:, 1, 0], v[5:, 1, 7] = 2.0 ** 127, -2.0 ** 126, 2.0 ** 127
+    T.run_prompt(q, k, v, [0, n], [0, n], rows={0, 1, 2, 10, 49, 127, 128, 399})
+
+
+@pytest.mark.parametrize("n,D", [(50, 64), (50, 128), (400, 64), (400, 128)])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_prompt_rows_without_weight_are_zero_whatever_the_values(n, D, bad):
+    rng = np.random.default_rng(62)
+    q, k, v = T.rand(rng, n, 4, D).abs() + 0.5, T.rand(rng, n, 2, D), T.rand(rng, n, 2, D)
+    k[:, 0] = -INF
+    k[:30, 1] = -INF
+    v[7], v[n - 2, :, 3] = bad, bad
+    T.run_prompt(q, k, v, [0, n], [0, n])
