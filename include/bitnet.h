@@ -467,9 +467,10 @@ BITNET_API bitnet_status bitnet_ffn_tp_finish(const int32_t* acc, int64_t M, int
  * key-value heads, query head h reads key-value head h / (Hq / Hkv).
  * Requires D = 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 64, Hq <= 65536.
  * Token strides are in elements, at least heads * D and multiples of 8 (so
- * that q, k and v may be slices of one fused projection).  scale is finite
- * and > 0.  Scores, maxima, sums and outputs are fp32; probabilities are
- * rounded to bf16 for the product with the values; y is rounded once.
+ * that q, k and v may be slices of one fused projection).  scale > 0, and
+ * scale * log2(e) is finite in fp32.  Scores, maxima, sums and outputs are
+ * fp32; probabilities are rounded to bf16 for the product with the values; y is
+ * rounded once.
  * A row that sees no key gives y = 0 and lse = -inf (likewise one whose
  * scores are all -inf).  Keys and values that a row does not see do not reach
  * it, whatever they hold (Inf and NaN included).

@@ -63,6 +63,10 @@ bool heads_ok(int64_t Hq, int64_t Hkv, int64_t D) {
   return (D == 64 || D == 128) && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 &&
          Hq / Hkv <= 64;
 }
+// A scale whose product with log2 e, by which the kernels multiply, is a number.
+bool scale_ok(float scale) {
+  return scale > 0.0f && std::isfinite((float)((double)scale * kLog2e));
+}
 bool stride_ok(int64_t stride, int64_t width) {
   return stride >= width && stride % 8 == 0 && stride <= kMaxI32;
 }
@@ -183,7 +187,7 @@ bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint
                                  int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale,
                                  uint16_t* y, int64_t y_stride, float* lse, void* stream) {
   if (!q || !k || !v || !cu_q || !cu_k || !y) return BITNET_ERR_INVALID_ARG;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return BITNET_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return BITNET_ERR_INVALID_ARG;
   if (B < 1 || B > kMaxI32 / 2 || Tq < 1 || Tq > kMaxI32 / 2 || Tk < 1 || Tk > kMaxI32 / 2 ||
       !heads_ok(Hq, Hkv, D) || !stride_ok(q_stride, Hq * D) || !stride_ok(y_stride, Hq * D) ||
       !stride_ok(k_stride, Hkv * D) || !stride_ok(v_stride, Hkv * D))
@@ -206,6 +210,7 @@ bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.y_stride = y_stride;
   a.B = (int)B; a.Tq = (int)Tq; a.Tk = (int)Tk;
   a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.group = (int)(Hq / Hkv);
+  a.scale = scale;
   a.scale_log2 = (float)((double)scale * kLog2e);
   // Very short prompts, few of them: the warp kernel starts faster (no tensor
   // memory, no tensor maps).  20 heads of 128, one prompt of 1 / 64 / 96 / 200
@@ -235,7 +240,7 @@ bitnet_status bitnet_attn_decode(const uint16_t* q, int64_t q_stride, const uint
   if (!q || !k_pages || !v_pages || !y) return BITNET_ERR_INVALID_ARG;
   bitnet_status st = check_tables(kv);
   if (st != BITNET_OK) return st;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return BITNET_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return BITNET_ERR_INVALID_ARG;
   if (B < 1 || B > kKvMaxSlots || (!slots && B > kv->n_slots) || !heads_ok(Hq, Hkv, D) ||
       !stride_ok(q_stride, Hq * D) || !stride_ok(y_stride, Hq * D))
     return BITNET_ERR_SHAPE;

@@ -26,7 +26,7 @@ struct AttnPromptArgs {
   int B, Tq, Tk, Hq, Hkv, group;
   int tile_tokens;        // tokens per tile
   int half_tokens;        // tile kernel: tokens per 128 rows
-  float scale_log2;       // scale * log2(e)
+  float scale, scale_log2;   // scale_log2 = scale * log2(e)
 };
 
 // One tile of work: rows [t0, t0 + n) of a sequence.
@@ -100,25 +100,30 @@ __device__ __forceinline__ float row_dot(const uint16_t* q, const uint16_t* k) {
   return dot;
 }
 
-// Mends one row of y, by one warp, where the tiled result is not finite though
-// the row's sum is a number.  There are three ways to that besides values that
-// the row sees.  A masked probability (0) times an infinite or NaN value of the
-// same sequence gives NaN: such a value is then among the masked keys that the
-// tile multiplied, [seen, n_end), and no NaN among the seen ones.  The sum of p v before the division can pass
-// fp32's range with values near its end: the column is then infinite without an
-// infinity of that sign among the seen values.  These columns are computed
-// again, in fp32 with the masked keys skipped and weights that are divided
-// first; all others stay.  And a row whose scores are all -inf (no_weight) is 0
-// whatever the values are.
-// Lane i has columns i D / 32 onwards.  4096 tokens of 20 heads (88 us): a NaN or
-// an infinity in a value that nearly all rows see 0.4 ms, all values NaN 0.6; an
-// infinity at position 2000 16 ms, a NaN there 10 and at position 4000 32 (the
-// rows just before it, few and long), a column of infinities 38.  Every such row
-// computed as a whole took 77 .. 92 ms, and so did rows that are NaN by a score,
-// which take no time now.
+// Mends one row of y, by one warp, where the tiled result is not finite.  There
+// are four ways to that besides values that the row sees.
+//  * A masked probability (0) times an infinite or NaN value of the same sequence
+//    gives NaN: such a value is then among the masked keys that the tile
+//    multiplied, [seen, n_end), and no NaN among the seen ones.
+//  * The sum of p v before the division passes fp32's range, with values near its
+//    end: the column is then infinite without an infinity of that sign among the
+//    seen values.  Columns of these two kinds are computed again, in fp32 with
+//    the masked keys skipped and weights that are divided first; others stay.
+//  * All scores are -inf (no_weight): the row is 0 whatever the values are.
+//  * The row's sum is NaN (whole).  A score that is NaN or +inf gives that, and the
+//    row stays NaN; and so do scores that the tile could not hold (see kPtFar),
+//    whose row and log-sum are computed from the start.
+// Lane i has columns i D / 32 onwards.
+// 4096 tokens of 20 heads (92 us): a NaN or an infinity in a value that nearly all
+// rows see 0.4 ms, all values NaN 0.6, a NaN key near the start or all queries NaN
+// 0.4; in the middle, a NaN key 9.5 ms, an infinite value 16, a NaN value 11, and
+// 35 at position 4000 (the rows just before it, few and long); a column of
+// infinities 38, all scores far from 0 30.  Computing every such row as a whole
+// took 77 .. 92 ms.
 template <int D>
 __device__ __noinline__ void prompt_row_by_warp(const AttnPromptArgs& a, const PromptTile& t,
-                                                int token, int head, int n_end, bool no_weight) {
+                                                int token, int head, int n_end, bool no_weight,
+                                                bool whole) {
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
   const int kvh = head / a.group;
@@ -147,6 +152,10 @@ __device__ __noinline__ void prompt_row_by_warp(const AttnPromptArgs& a, const P
     nans |= (uint32_t)((y[i] & 0x7fffu) > 0x7f80u) << i;
     infs |= (uint32_t)((y[i] & 0x7fffu) == 0x7f80u) << i;
   }
+  if (whole) {
+    nans = infs = 0;
+    found = ~0u;
+  }
   if (__any_sync(0xffffffffu, nans != 0)) {
 #pragma unroll 8
     for (int j = seen; j < n_end; ++j) {
@@ -169,25 +178,28 @@ __device__ __noinline__ void prompt_row_by_warp(const AttnPromptArgs& a, const P
         found |= (uint32_t)(infs >> i & 1u ? x[i] == y[i] : (x[i] & 0x7fffu) > 0x7f80u) << i;
     }
   }
-  need &= ~found;
+  need = whole ? ~0u : need & ~found;
   if (!__any_sync(0xffffffffu, need != 0)) return;
+  const float c = a.scale_log2;
   float m = -INFINITY, l = 0.f, o[V];
   for (int j0 = 0; j0 < seen; j0 += 32) {
-    const float s = j0 + lane < seen ? row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) * a.scale_log2
-                                     : -INFINITY;
+    const float s = j0 + lane < seen ? row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) : -INFINITY;
     const float top = fmaxf(m, warp_max(s));
-    l = l * (m == top ? 1.f : ex2(m - top)) + ex2(s - (top == -INFINITY ? 0.f : top));
+    if (__any_sync(0xffffffffu, !(s < INFINITY))) return;   // NaN, as it stands
+    l = l * (m == top ? 1.f : ex2((m - top) * c)) + ex2((s - (top == -INFINITY ? 0.f : top)) * c);
     m = top;
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   const float inv = 1.f / l;
+  if (whole && a.lse && lane == 0)
+    a.lse[(int64_t)(t.q0 + token) * a.Hq + head] = fmaf(m, a.scale, logf(l));
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
   for (int j0 = 0; j0 < seen; j0 += 32) {
     float p = 0.f;
     if (j0 + lane < seen)
-      p = ex2(row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) * a.scale_log2 - m) * inv;
+      p = ex2((row_dot<D>(q, k + (int64_t)(j0 + lane) * a.k_stride) - m) * c) * inv;
     for (int x0 = 0; x0 < 32; x0 += 8) {     // eight rows of values on their way
       uint32_t w[8][V] = {};
 #pragma unroll
@@ -302,7 +314,7 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int key = j * kPwKeys + nt * 8 + 2 * (lane & 3) + (e & 1);
-        s[nt][e] = key <= (e < 2 ? lim0 : lim1) && key < n_keys ? s[nt][e] * a.scale_log2 : -INFINITY;
+        s[nt][e] = key <= (e < 2 ? lim0 : lim1) && key < n_keys ? s[nt][e] : -INFINITY;
         if (e < 2) t0 = fmaxf(t0, s[nt][e]); else t1 = fmaxf(t1, s[nt][e]);
       }
 #pragma unroll
@@ -312,7 +324,8 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
     }
     t0 = fmaxf(t0, m[0]);
     t1 = fmaxf(t1, m[1]);
-    const float f0 = m[0] == t0 ? 1.f : ex2(m[0] - t0), f1 = m[1] == t1 ? 1.f : ex2(m[1] - t1);
+    const float c = a.scale_log2;
+    const float f0 = m[0] == t0 ? 1.f : ex2((m[0] - t0) * c), f1 = m[1] == t1 ? 1.f : ex2((m[1] - t1) * c);
     m[0] = t0;
     m[1] = t1;
     l[0] *= f0;
@@ -327,10 +340,10 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
     const float z0 = t0 == -INFINITY ? 0.f : t0, z1 = t1 == -INFINITY ? 0.f : t1;
 #pragma unroll
     for (int nt = 0; nt < kPwKeys / 8; ++nt) {
-      s[nt][0] = ex2(s[nt][0] - z0);
-      s[nt][1] = ex2(s[nt][1] - z0);
-      s[nt][2] = ex2(s[nt][2] - z1);
-      s[nt][3] = ex2(s[nt][3] - z1);
+      s[nt][0] = ex2((s[nt][0] - z0) * c);
+      s[nt][1] = ex2((s[nt][1] - z0) * c);
+      s[nt][2] = ex2((s[nt][2] - z1) * c);
+      s[nt][3] = ex2((s[nt][3] - z1) * c);
       l[0] += s[nt][0] + s[nt][1];
       l[1] += s[nt][2] + s[nt][3];
     }
@@ -369,9 +382,8 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
         *reinterpret_cast<uint32_t*>(yr + i * 8 + 2 * (lane & 3)) = pack_bf16(x0, x1);
       }
       if (a.lse && (lane & 3) == 0)
-        a.lse[token * a.Hq + head] = l[half] == 0.f
-                                         ? -INFINITY
-                                         : (m[half] + log2f(l[half])) * 0.69314718055994531f;
+        a.lse[token * a.Hq + head] =
+            l[half] == 0.f ? -INFINITY : fmaf(m[half], a.scale, logf(l[half]));
     }
     // a sum that is NaN makes the whole row NaN, which it is already
     unsigned nan = __ballot_sync(0xffffffffu, odd != odd && l[half] == l[half]);
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
     const int r = warp * 16 + (bit >> 2) + 8 * (bit & 3);
     __syncwarp();
     prompt_row_by_warp<D>(a, t, t.t0 + r / a.group, kvh * a.group + r % a.group, n_keys,
-                          none >> bit & 1u);
+                          none >> bit & 1u, false);
   }
 }
 
@@ -439,6 +451,15 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
 constexpr int kPtKeys = 128, kPtSub = 64;
 constexpr int kPtThreads = 640;
 constexpr int kPtRegs = 96;                  // 65536 / 640, in steps of 8
+// The exponents are fma(s, c, -(c m)) with c m rounded before.  That rounding
+// is the same for the whole row and leaves its result while it is small against
+// fp32's range of exponents: at most 32 below |c m| = 2^30.  Rows whose
+// reference was ever farther from 0 get NaN as their sum and are computed again
+// by prompt_row_by_warp, which subtracts first.  Doing that here costs every step
+// of every row: 4096 tokens of 20 heads 92 -> 98 us with the subtraction, 95 with
+// a second loop for such rows, 94 with a factor c per row that makes the product
+// exact.
+constexpr float kPtFar = 1073741824.0f;
 template <int D>
 struct PtCfg {
   static constexpr int kHalves = D / 64;                  // 128-byte wide column blocks
@@ -887,6 +908,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               tmem_st32_async(ot + x, o);
             }
           }
+          if (fabsf(m) < INFINITY && !(fabsf(m * c) < kPtFar)) l2[0] = f2_pack(NAN, NAN);
           continue;
         }
         tmem_st16_async(pt + sub, p);
@@ -965,21 +987,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             l == 0.0f ? -INFINITY
                       : ((m == -INFINITY ? 0.0f : m * c) + log2f(l)) * 0.69314718055994531f;
     }
-    // rows with a result that is not finite and a sum that is a number are looked
-    // at again, the pair's warps taking turns; both warps' stores come first.  (A
-    // sum that is NaN makes the whole row NaN, which it is already.)
-    const bool mend = ok && r < rows && l == l && odd != odd;
+    // rows with a result that is not finite are looked at again, the pair's warps
+    // taking turns; both warps' stores come first
+    const bool mend = ok && r < rows && odd != odd;
     if (pair_any(pair, mend)) {
       *mine = mend ? 1.0f : 0.0f;
       pair_sync(pair);
       unsigned redo = __ballot_sync(0xffffffffu, *mine + *other > 0.0f);
       const unsigned none = __ballot_sync(0xffffffffu, l == 0.0f);
+      const unsigned whole = __ballot_sync(0xffffffffu, l != l);
       for (int k = 0; redo; ++k) {
         const int bit = __ffs(redo) - 1, row = r0 + bit;
         redo &= redo - 1;
         if ((k & 1) == cg)
           prompt_row_by_warp<D>(a, t, first + row / a.group, kvh * a.group + row % a.group,
-                                min(n * kPtSub, t.kl), none >> bit & 1u);
+                                min(n * kPtSub, t.kl), none >> bit & 1u, whole >> bit & 1u);
       }
     }
   }

@@ -143,6 +143,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         B.bitnet_kv_copy_pages([], [], c, c)
 
 
+def test_scales_whose_product_with_log2_e_is_not_finite(L):
+    need = L.bitnet_attn_decode_workspace_size(1, 8, 8, 64)
+    for s in (2.5e38, 3.4e38, -2.5e38):
+        assert L.bitnet_attn_prompt(P[0], 512, P[1], 512, P[2], 512, P[3], P[4], 1, 9, 9, 8, 8, 64, s, P[5], 512, None, None) == 1
+        assert L.bitnet_attn_decode(P[0], 512, P[1], P[2], kv(), None, 1, 8, 8, 64, s, P[5], 512, None, P[6], need, None) == 1
+
+
 def test_binding_refuses_host_pages_and_pools_of_host_buffers(monkeypatch):
     """Tensors that are all on the host agree with each other about their device; no pointer of theirs may reach the
     library."""

@@ -12,6 +12,7 @@ from tests import test_gpu_attention as T
 
 pytestmark = pytest.mark.gpu
 
+BF = torch.bfloat16
 NAN, INF = float("nan"), float("inf")
 
 
@@ -139,6 +140,98 @@ def test_fork_of_long_parents():
     got, n = B.bitnet_kv_fork(pool, T.i32(par), T.i32(kids), short_pages=short)
     assert want == 0 and int(short) == 0 and got[:int(n)].tolist() == [list(p) for p in pairs]
     T.same_tables(pool, host)
+
+
+# ------------------------------------------------------------- scores
+def check_far(y, lse, q, keys, vals, scale, where):
+    """A row whose q . k are exact in fp32 (small integers).  What the kernels round then is the exponent: scale * log2 e,
+    the difference of two scores where they are not close, and its product, half a step each, and 2^-22 of the exponential;
+    a key whose exponent is below -40 has no weight that shows.  Sums of n terms add n U_SUM, a weight half a bf16 step.
+    The log-sum adds two rounded products of the scale."""
+    n = len(keys)
+    s = keys @ q * scale
+    top = s.max()
+    p = np.exp(s - top)
+    total = p.sum()
+    rel = 40 * 3 * 2.0 ** -24 + 2.0 ** -22 + (n + 8) * A.U_SUM
+    want = (p[:, None] * vals).sum(0) / total
+    spread = (p[:, None] * np.abs(vals)).sum(0) / total
+    assert np.all(np.abs(y - want) <= spread * (A.U_BF16 + 2 * rel) * 1.01 + np.abs(want) * A.U_BF16), where
+    if abs(top) < 3.402e38:                                          # fp32 ends at 3.4028e38
+        assert abs(lse - (top + np.log(total))) <= abs(top) * 2.0 ** -22 + rel + 2.0 ** -20, (where, lse, top)
+    elif abs(top) > 3.404e38:
+        assert lse == np.sign(top) * np.inf, (where, lse, top)
+
+
+SCALES = [2.0 ** 20, 2.0 ** 26, 1.5e9, 2.0 ** 34, 1e12, 1e20, 1e30, 2e36, 2.3e38]
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,D", [(40, 64), (40, 128), (400, 64), (400, 128)])       # both sides of the dispatch rule
+def test_prompt_scores_far_from_zero(n, D, sign, scale):
+    """The largest score is far from 0, above or below: the row is the mean of the values of the keys that share it."""
+    rng = np.random.default_rng(50)
+    scale = float(np.float32(scale))
+    q = torch.from_numpy(rng.integers(1, 4, (n, 4, D))).to(BF)
+    k = torch.from_numpy(sign * rng.integers(0, 4, (n, 2, D))).to(BF)
+    k[:, 0] = k[torch.from_numpy(rng.integers(0, 6, n)), 0]          # ties
+    k[0, 0, 0] = k[0, 1, 0] = sign * 3.0
+    v = T.rand(rng, n, 2, D)
+    y, lse = B.bitnet_attn_prompt(q.cuda(), k.cuda(), v.cuda(), T.i32([0, n]), scale=scale, want_lse=True)
+    yh, lh = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    qh, kh, vh = T.f64(q), T.f64(k), T.f64(v)
+    for t in range(0, n, 1 if n < 100 else 7):
+        for h in range(4):
+            check_far(yh[t, h], lh[t, h], qh[t, h], kh[:t + 1, h // 2], vh[:t + 1, h // 2], scale, (t, h))
+
+
+@pytest.mark.parametrize("scale", SCALES[:-2])                     # scale * q . k stays in fp32's range
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("lens,heads", [([5, 70, 1, 400], (4, 2, 64)), ([20000, 3], (20, 2, 128))])
+def test_decode_scores_far_from_zero(lens, heads, sign, scale):
+    rng = np.random.default_rng(51)
+    Hq, Hkv, D = heads
+    scale = float(np.float32(scale))
+    pool, host, kp, vp, ks, vs = T.make_cache(rng, lens, 64, Hkv, D)
+    for b, n in enumerate(lens):
+        ks[b] = torch.from_numpy(sign * rng.integers(0, 4, (n, Hkv, D))).to(BF)
+        ks[b][:, 0] = ks[b][torch.from_numpy(rng.integers(0, min(n, 6), n)), 0]
+        ks[b][0, :, 0] = sign * 3.0
+        for i in range(-(-n // 64)):
+            rows = min(64, n - i * 64)
+            kp[int(host.table[b, i]), :, :rows] = ks[b][i * 64:i * 64 + rows].transpose(0, 1).cuda()
+    q = torch.from_numpy(rng.integers(1, 4, (len(lens), Hq, D))).to(BF)
+    y, lse = B.bitnet_attn_decode(q.cuda(), kp, vp, pool, scale=scale, want_lse=True)
+    yh, lh = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(len(lens)):
+        kh, vh = T.f64(ks[b]), T.f64(vs[b])
+        for h in range(0, Hq, 3):
+            g = h // (Hq // Hkv)
+            check_far(yh[b, h], lh[b, h], T.f64(q[b, h]), kh[:, g], vh[:, g], scale, (b, h))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_prompt_scores_far_from_zero_and_keys_that_are_not_finite(D, bad):
+    """Rows that see the key and rows that do not, scores that come from far below 0 to near it, and back up."""
+    rng = np.random.default_rng(52)
+    n = 400
+    q = torch.ones(n, 2, D, dtype=BF)
+    k = torch.zeros(n, 1, D, dtype=BF)
+    k[:, 0, 0] = torch.tensor([-2.0 ** 34] * 70 + [-2.0 ** 33] * 70 + [-3.0] * 70 + [1.0] * 70 + [2.0 ** 35] * 50 + [0.0] * 70)
+    k[360, 0, 1] = bad
+    v = T.rand(rng, n, 1, D)
+    y, lse = B.bitnet_attn_prompt(q.cuda(), k.cuda(), v.cuda(), T.i32([0, n]), scale=1.0, want_lse=True)
+    yh, lh = y.double().cpu().numpy(), lse.double().cpu().numpy()
+    kh, vh = T.f64(k), T.f64(v)
+    kh[360, 0, 1] = -np.inf if bad == -INF else 0.0      # no weight for the rows that are checked, or not seen by them
+    for t in list(range(0, n if bad == -INF else 360, 3)):
+        for h in range(2):
+            seen = [j for j in range(t + 1) if j != 360]
+            check_far(yh[t, h], lh[t, h], np.ones(D), kh[seen, 0], vh[seen, 0], 1.0, (t, h))
+    if bad != -INF:
+        assert np.isnan(yh[360:]).all()
 
 
 # ------------------------------------------------ values that are not finite
