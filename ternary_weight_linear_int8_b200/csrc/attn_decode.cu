@@ -392,9 +392,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, dec_ctas<D>()) attn_decode_ker
         const float* w1 = w0 + 8 * NT * (D + 4);
         const float x0 = w0[0] + w1[0], x1 = w0[1] + w1[1];
         if (whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          *reinterpret_cast<uint32_t*>(a.y + (int64_t)cur.b * a.y_stride +
-                                       (int64_t)(head0 + h) * D + d) = pack_bf16(x0 * inv, x1 * inv);
+          // no weight (all scores -inf): 0, whatever the values are
+          const float inv = 1.f / sum;
+          *reinterpret_cast<uint32_t*>(a.y + (int64_t)cur.b * a.y_stride + (int64_t)(head0 + h) * D +
+                                       d) = sum == 0.f ? 0u : pack_bf16(x0 * inv, x1 * inv);
           if (a.lse && d == 0)
             a.lse[(int64_t)cur.b * a.Hq + head0 + h] =
                 sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
@@ -506,10 +507,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnDecodeArgs a, 
     }
     top = all;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = 1.f / sum;
 #pragma unroll
   for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(yr + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(yr + i) =
+        sum == 0.f ? 0u : pack_bf16(acc[i] * inv, acc[i + 1] * inv);
   if (a.lse && lane == 0)
     a.lse[id] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }

@@ -285,3 +285,26 @@ def test_prompt_rows_without_weight_are_zero_whatever_the_values(n, D, bad):
     k[:30, 1] = -INF
     v[7], v[n - 2, :, 3] = bad, bad
     T.run_prompt(q, k, v, [0, n], [0, n])
+
+
+@pytest.mark.parametrize("lens", [[70, 3], [9000, 64]])            # one block a head, and joined ones
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_decode_rows_without_weight_are_zero_whatever_the_values(lens, bad):
+    rng = np.random.default_rng(63)
+    Hq, Hkv, D = 8, 2, 64
+    pool, host, kp, vp, ks, vs = T.make_cache(rng, lens, 16, Hkv, D)
+    kp[:, 0] = -INF
+    ks = [k.clone() for k in ks]
+    for k in ks:
+        k[:, 0] = -INF
+    for b, n in enumerate(lens):
+        at = n // 2
+        vs[b][at] = bad
+        vp[int(host.table[b, at // 16]), :, at % 16] = bad
+    q = T.rand(rng, 2, Hq, D).abs() + 0.5
+    y, lse = B.bitnet_attn_decode(q.cuda(), kp, vp, pool, want_lse=True)
+    yh, lh = y.double().cpu().numpy(), lse.cpu().numpy()
+    for b in range(2):
+        for h in range(Hq):
+            T.check_row(yh[b, h], lh[b, h], A.row(T.f64(q[b, h]), T.f64(ks[b][:, h // 4]), T.f64(vs[b][:, h // 4]), D ** -0.5),
+                        (b, h))
