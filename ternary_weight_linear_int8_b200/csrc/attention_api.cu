@@ -213,12 +213,18 @@ bitnet_status bitnet_attn_prompt(const uint16_t* q, int64_t q_stride, const uint
   a.scale = scale;
   a.scale_log2 = (float)((double)scale * kLog2e);
   // Very short prompts, few of them: the warp kernel starts faster (no tensor
-  // memory, no tensor maps).  20 heads of 128, one prompt of 1 / 64 / 96 / 200
-  // tokens: 4.3 / 6.0 / 7.4 / 9.4 us against the tile kernel's 5.8 / 6.2 / 6.7 /
-  // 7.8; 16 heads of 64, 64 / 128 / 200 / 300 tokens: 4.3 / 5.2 / 6.4 / 7.9
-  // against 5.0 / 6.4 / 6.7 / 7.6.
-  const bool few = prompt_ctas(a, kPwRows / a.group) * 2 <= 3 * d.num_sms &&
-                   Tk <= (D == 64 ? 192 : 64) * B;
+  // memory, no tensor maps).  20 heads of 128, one prompt of 32 / 64 / 96 / 192
+  // tokens: 6.1 / 6.3 / 7.5 / 9.0 us against the tile kernel's 6.3 / 6.4 / 7.1 /
+  // 7.6; 16 heads of 64, 64 / 128 / 192 / 256 tokens: 4.5 / 5.4 / 6.4 / 7.3 against
+  // 5.5 / 6.2 / 6.3 / 7.0.  The lengths are on the device, so several sequences
+  // may be one long one and empty ones: the sum is held where that costs less
+  // than equal lengths gain.  20 sequences of 128 tokens in all, 12 heads of 128:
+  // equal 5.8 against 6.6, one of 128 7.4 against 6.8 (of 512: 6.2 / 7.0, 16.1 /
+  // 10.5); of 256 in all, 8 heads of 64: 4.7 / 5.8 and 7.6 / 7.1 (of 768: 4.7 / 5.7,
+  // 15.4 / 11.6).
+  const int64_t each = D == 64 ? 192 : 64, all = D == 64 ? 256 : 128;
+  const bool few = prompt_ctas(a, kPwRows / a.group) * 2 <= 3 * d.num_sms && Tk <= all &&
+                   Tk <= each * B;
   if (few)
     return D == 64 ? prompt_warp_launch<64>(a, as_stream(stream))
                    : prompt_warp_launch<128>(a, as_stream(stream));
