@@ -144,6 +144,13 @@ template <int D>
 bitnet_status prompt_tile_launch(AttnPromptArgs a, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   constexpr size_t smem = PtCfg<D>::kSmem;
+  // The kernel's softmax warps ask for kPtRegs registers; a build that launches
+  // it with fewer would have them wait for registers that no warp gives back.
+  static const bool regs_ok = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, prompt_tile_kernel<D>) == cudaSuccess && f.numRegs >= kPtRegs;
+  }();
+  if (!regs_ok) return BITNET_ERR_UNSUPPORTED;
   if (set_smem_attr_once(configured, prompt_tile_kernel<D>, (int)smem) != cudaSuccess)
     return BITNET_ERR_CUDA;
   const int half = 128 / a.group;

@@ -818,10 +818,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
-    // The registers the launch gave (no more are asked for).  Without the
-    // statement the compiler schedules the loop below worse: 4096 tokens of 20
-    // heads 91.8 instead of 87.9 us.  Giving the softmax warps 104 and the others
-    // 64 spills in the issuing thread: 98 us.
+    // The registers the launch gave (no more are asked for; the host checks that
+    // the build has them).  Without the statement the compiler schedules the loop
+    // below worse: 4096 tokens of 20 heads 91.8 instead of 87.9 us.  Giving the
+    // softmax warps 104 and the others 64 spills in the issuing thread: 98 us.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegs));
     const int i = warp >> 3, cg = (warp >> 2) & 1;       // row half, column half
     const int r = 32 * (warp & 3) + lane;    // this thread's row
