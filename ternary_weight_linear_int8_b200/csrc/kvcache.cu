@@ -337,7 +337,12 @@ __global__ void __launch_bounds__(256) kv_free_kernel(KvTables kv, const int32_t
     if (*t >= 0) {
       const int page = atomicExch(t, -1);
       if (page >= 0) {
-        if (page >= kv.n_pages || atomicSub(&kv.refs[page], 1) <= 0) record_error(BITNET_ERR_PAGES);
+        if (page >= kv.n_pages) {
+          record_error(BITNET_ERR_PAGES);
+        } else if (atomicSub(&kv.refs[page], 1) <= 0) {   // no count held the entry: it stays free
+          atomicAdd(&kv.refs[page], 1);
+          record_error(BITNET_ERR_PAGES);
+        }
       }
     }
     if (e == 0) kv.lens[s] = 0;

@@ -142,6 +142,23 @@ def test_fork_of_long_parents():
     T.same_tables(pool, host)
 
 
+def test_free_of_entries_that_no_count_holds():
+    """Damaged tables: pages that are named more often than counted.  Their counts end at 0 and they can be taken again."""
+    rng = np.random.default_rng(45)
+    pool, host, _, _, _, _ = T.make_cache(rng, [40, 20, 16], 16, 1, 64, spare=3, max_pages=4)
+    pool.refs[int(host.table[0, 1])] = 0
+    pool.table[1, 0] = int(host.table[0, 2])                     # named twice, counted once
+    pool.refs[int(host.table[1, 0])] = 0
+    B.bitnet_kv_free(pool, T.i32([0, 1]))
+    assert B.bitnet_last_device_status() == 9
+    left = torch.zeros(len(host.refs), dtype=torch.int32)
+    left[int(host.table[2, 0])] = 1
+    assert torch.equal(pool.refs.cpu(), left)
+    short = T.i32([77])
+    B.bitnet_kv_extend(pool, T.i32([64, 64]), slots=T.i32([0, 1]), short_pages=short)
+    assert int(short) == 0 and bool((pool.refs == 1).all())
+
+
 # ------------------------------------------------------------- scores
 def check_far(y, lse, q, keys, vals, scale, where):
     """A row whose q . k are exact in fp32 (small integers).  What the kernels round then is the exponent: scale * log2 e,
