@@ -555,8 +555,12 @@ BITNET_API bitnet_status bitnet_kv_extend(const bitnet_kv_tables* kv, const int3
  * position lens[slot] - (cu[b+1] - cu[b]) + r - cu[b].  Call it after
  * bitnet_kv_extend, once per layer.  cu [B+1] int32 on the device does not
  * decrease; rows outside all sequences are not read.  Rows without a valid
- * slot, position or page are skipped (BITNET_ERR_PAGES).  A slot named twice
- * gets the rows of one of the two.  Pages shared by several sequences are
+ * slot, position or page are skipped (BITNET_ERR_PAGES).  A refused
+ * bitnet_kv_extend leaves lens as it was, and an append that follows it all the
+ * same overwrites the newest rows: look at short_pages first, or, in a captured
+ * step, let slots be -1 where it is not 0 (such rows are skipped).  Where a slot
+ * is named twice, each 16 bytes are those of one of the two rows, it is not said
+ * which.  Pages shared by several sequences are
  * written as they are: bitnet_kv_fork shares full pages only, so appended
  * rows never meet one.  The pages may not overlap each other, k or v.
  */
@@ -572,7 +576,8 @@ BITNET_API bitnet_status bitnet_kv_append(const uint16_t* k, int64_t k_stride, c
  * slots[b] (NULL: b; a slot may be read by several rows).
  * q, y [B, Hq, D] with row strides q_stride, y_stride; lse [B, Hq] or NULL.
  * A slot or length outside the tables counts as empty, a page outside the
- * pool as keys that are not seen (BITNET_ERR_PAGES).
+ * pool as keys that are not seen (BITNET_ERR_PAGES).  The values are summed
+ * before the division: |v| times the number of keys stays below 2^128.
  * workspace  >= bitnet_attn_decode_workspace_size(B, Hq, Hkv, D) bytes.
  * 1 <= B <= 65536.  y may not overlap q or the pages.
  */
@@ -624,7 +629,7 @@ BITNET_API bitnet_status bitnet_kv_compact(const bitnet_kv_tables* kv, int32_t* 
 
 /*
  * Copy pages inside the caches of L layers: for each of the first *n_pairs
- * pairs (at most max_pairs are read) page pairs[i][0] to page pairs[i][1],
+ * pairs (at most max_pairs <= n_pages are read) page pairs[i][0] to page pairs[i][1],
  * keys and values.  k_pages, v_pages: HOST arrays of L device pointers, read
  * during the call only; page_bytes = Hkv * page_size * D * 2, a multiple of
  * 16.  No destination may be named twice or also be a source (lists from

@@ -23,7 +23,7 @@
 //   O^T [D x 8 heads]        += V^T P^T       V by ldmatrix.trans
 // Keys are the M side because groups have at most 8 heads as a rule, so that
 // the heads fill the 8-wide N side; P^T is S^T's accumulator transposed in
-// registers (movmatrix).  P is rounded to bf16 for the second product (2^-9
+// registers (movmatrix).  P is rounded to bf16 for the second product (2^-8
 // relative at most, like the outputs' own rounding); maxima, sums and
 // outputs stay in fp32.
 #include "attention.cuh"

@@ -432,16 +432,20 @@ __global__ void __launch_bounds__(128, 2) prompt_warp_kernel(const AttnPromptArg
 // O_i rescaled.  bf16 has fp32's range, so probabilities up to 2^8 lose
 // nothing.
 //
-// Measured (device time): 4096 tokens of 20 heads of 128 on 4 key-value heads
-// 88 us (977 TFLOP/s), 16384 tokens 1.19 ms (1158, power capped), 4096 tokens of
-// 16 heads of 64 71 us.  A step of both halves takes about 1850 cycles with
-// D = 128.  Its MMAs back to back take 1239 (the score MMAs read Q and K from
-// shared memory at its full 128 bytes a clock, so 48 cycles instead of 32 for
-// 128 x 64 x 16); with the barriers handed over but no softmax 1560; taking the
-// ring's TMA traffic away changes nothing.  The four softmax warps of a
-// scheduler need 1024 cycles for the exponentials alone (4 a clock), which
-// is the bound with D = 64.  What the issuing thread does between MMAs counts:
-// its loop is unrolled over halves and steps, one thread issues everything.
+// Measured (device time, the same inputs again and again): 4096 tokens of 20
+// heads of 128 on 4 key-value heads 90 us (955 TFLOP/s; 103 on inputs that
+// change from call to call), 16384 tokens 1.14 ms, 1.31 under the power cap
+// (1200, 1050), 4096 tokens of 16 heads of 64 61 us.  Every CTA searches its
+// tile in the bounds, 32 sequences at a time, which shows with hundreds of
+// them: 200 prompts of 32 tokens 75 us, 1000 of them 709.  A step of both
+// halves takes about 1850 cycles with D = 128.  Its MMAs back to back take 1239
+// (the score MMAs read Q and K from shared memory at its full 128 bytes a
+// clock, so 48 cycles instead of 32 for 128 x 64 x 16); with the barriers
+// handed over but no softmax 1560; taking the ring's TMA traffic away changes
+// nothing.  The four softmax warps of a scheduler need 1024 cycles for the
+// exponentials alone (4 a clock), which is the bound with D = 64.  What the
+// issuing thread does between MMAs counts: its loop is unrolled over halves and
+// steps, one thread issues everything.
 // Alternatives, 4096 tokens of 20 heads: scores 128 keys wide and single
 // buffered (a half's softmax and MMAs in turn) 97 us; one thread per whole row
 // (8 softmax warps) 105 us and more; two issuing warps, one per half (the
