@@ -142,6 +142,41 @@ def test_fork_of_long_parents():
     T.same_tables(pool, host)
 
 
+def test_append_after_a_refused_extend_is_skipped_by_slots_of_minus_one():
+    """A captured step whose slots become -1 on the device where the extend was refused: nothing that is held changes."""
+    rng = np.random.default_rng(46)
+    pool, host, kp, vp, _, _ = T.make_cache(rng, [31, 16], 16, 2, 64, spare=1, poison=2.0, max_pages=4)
+    ids, one, c, short = T.i32([0, 1]), T.i32([1, 1]), T.i32([0, 1, 2]), T.i32([0])
+    k = T.rand(rng, 2, 2, 64).cuda()
+
+    def step():
+        B.bitnet_kv_extend(pool, one, short_pages=short)
+        B.bitnet_kv_append(k, -k, c, pool, kp, vp, slots=torch.where(short == 0, ids, -1).to(torch.int32))
+
+    side = torch.cuda.Stream()
+    keep = pool.buf.clone(), kp.clone(), vp.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()
+        for t, u in zip((pool.buf, kp, vp), keep):
+            t.copy_(u)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for granted in (True, False):                                # slot 1 takes the last page, then slot 0 wants one
+        graph.replay()
+        assert (host.extend([1, 1]) == 0) == granted
+        assert B.bitnet_last_device_status() == (0 if granted else 9) and (int(short) == 0) == granted
+        T.same_tables(pool, host)
+        if granted:
+            held = kp.clone(), vp.clone()
+            for b, n in ((0, 32), (1, 17)):
+                assert torch.equal(kp[int(host.table[b, (n - 1) // 16]), :, (n - 1) % 16], k[b])
+            k.copy_(T.rand(rng, 2, 2, 64))
+    assert torch.equal(kp, held[0]) and torch.equal(vp, held[1])
+
+
 def test_free_of_entries_that_no_count_holds():
     """Damaged tables: pages that are named more often than counted.  Their counts end at 0 and they can be taken again."""
     rng = np.random.default_rng(45)
@@ -371,3 +406,19 @@ def test_prompt_one_long_sequence_among_empty_ones_is_no_slower(heads, n):
             t.append(a.elapsed_time(b))
     one, many = (min(t) for t in times)
     assert many < 1.35 * one, (one, many)
+
+
+def test_binding_without_the_private_names_of_torch(monkeypatch):
+    """The public calls that stand in for them give the same stream and device."""
+    rng = np.random.default_rng(64)
+    q, k, v = (T.rand(rng, 90, h, 64).cuda() for h in (4, 2, 2))
+    c = T.i32([0, 40, 90])
+    want = B.bitnet_attn_prompt(q, k, v, c)[0]
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    monkeypatch.setattr(B, "_current_device", torch.cuda.current_device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = B.bitnet_attn_prompt(q, k, v, c)[0]
+    side.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
